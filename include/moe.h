@@ -439,6 +439,172 @@ MOE_API int32_t moe_abi_version(void);
  */
 MOE_API moe_status moe_selftest_bounded_wait(int64_t timeout_ns, moe_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Training the routed experts in 8 bits.  No page counterpart: the pages
+ * describe inference; these entry points are the products, checkpoints and
+ * gradients that fine-tuning the same layer needs next to it.
+ *
+ * Rows are grouped by expert as moe_permute leaves them: rows
+ * offsets[e] .. offsets[e+1] - 1 belong to expert e, offsets [E+1] int32 on
+ * the device.  Offsets outside [0, R], or decreasing ones, are clamped and
+ * flag MOE_ERR_DEVICE_BOUNDS.  A block is 128 consecutive columns of a row
+ * (rows x: one fp32 scale per block, scales [rows, ceil(cols/128)]) or 128 x
+ * 128 of a weight matrix; the last block of a row or matrix may be shorter.
+ * Limits: E <= 1024, R <= 2^24.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum moe_scale_kind {
+  MOE_SCALE_AMAX = 0, /* s = a / 448, correctly rounded                       */
+  MOE_SCALE_POW2 = 1  /* s = 2^p with a / 2^p in (224, 448]                   */
+} moe_scale_kind;
+
+/*
+ * moe_quantize_blocks_e4m3 -- rows as E4M3 codes with a scale per block.
+ *
+ *   a         = largest finite |x| of the block, at least 2^-100
+ *               (s = 1 when every finite value of the block is zero)
+ *   code[r,i] = E4M3(x[r,i] * t): nearest E4M3 value, ties to the even code;
+ *               t = 448 / a correctly rounded (MOE_SCALE_AMAX), t = 1 / s
+ *               exactly (MOE_SCALE_POW2)
+ * Infinities and NaN become the NaN code and do not enter the scale.  Codes
+ * and scales are exact functions of the inputs (bit-reproducible).  With
+ * MOE_SCALE_POW2 code * s is exactly a bf16 value: the form to keep rows in
+ * for moe_grouped_wgrad.
+ *
+ *   x       [rows, cols] x_dtype (MOE_BF16 or MOE_F32), row pitch ld_x
+ *           elements (>= cols; rows 16-byte aligned)
+ *   codes   [rows, cols] uint8 out      scales [rows, ceil(cols/128)] fp32 out
+ * cols % 8 == 0, else MOE_ERR_UNSUPPORTED.  rows == 0: nothing is enqueued.
+ */
+MOE_API moe_status moe_quantize_blocks_e4m3(int32_t rows, int32_t cols, int32_t x_dtype, int32_t scale_kind,
+                                            const void *x, int64_t ld_x, uint8_t *codes, float *scales,
+                                            moe_stream_t stream);
+
+/*
+ * moe_grouped_block_gemm -- E4M3 rows times E4M3 weights, both with scales
+ * per block of 128 along the reduction.  For every row r of expert e:
+ *
+ *   out[r,n] = sum_kb a_scales[r,kb] * w_scales[e,n/128,kb] *
+ *              sum_{i in block kb} a[r,i] * w[e,n,i]
+ *
+ * products exact, sums and scales in fp32, rounded once to out_dtype.
+ *   a_codes [R, K]   a_scales [R, ceil(K/128)]
+ *   transposed == 0: w_codes [E, N, K], w_scales [E, ceil(N/128), ceil(K/128)]
+ *   transposed != 0: w_codes [E, K, N], w_scales [E, ceil(K/128), ceil(N/128)]
+ *     -- the data gradient of the product above on the same arrays: call with
+ *     K the forward's output channels and N its input channels
+ *   out [R, N] MOE_BF16 or MOE_F32
+ * Any fp32 scales are accepted.  K % 16 == 0 and N % 16 == 0, else
+ * MOE_ERR_UNSUPPORTED.  Rows outside every expert's range are left untouched;
+ * R == 0: nothing is enqueued.
+ */
+MOE_API moe_status moe_grouped_block_gemm(int32_t R, int32_t K, int32_t N, int32_t E, int32_t transposed,
+                                          int32_t out_dtype, const uint8_t *a_codes, const float *a_scales,
+                                          const int32_t *offsets, const uint8_t *w_codes,
+                                          const float *w_scales, void *out, moe_stream_t stream);
+
+/*
+ * moe_swiglu_save_e4m3 -- h = SiLU(g) * u, keeping g and u in 8 bits.
+ *
+ *   g, u          [R, ffn] bf16, row pitch ld elements each (the halves of one
+ *                 [R, 2 ffn] product: u = g + ffn, ld = 2 ffn)
+ *   h             [R, ffn] bf16 out, or NULL
+ *   h_codes       [R, ffn], h_scales [R, ceil(ffn/128)] out, or both NULL: h
+ *                 in blocks with MOE_SCALE_AMAX, from h in fp32
+ *   saved_codes   [2, R, ffn], saved_scales [2, R, ceil(ffn/128)] out: g, then
+ *                 u, as moe_quantize_blocks_e4m3 with MOE_SCALE_POW2
+ * ffn % 16 == 0, else MOE_ERR_UNSUPPORTED.
+ */
+MOE_API moe_status moe_swiglu_save_e4m3(int32_t R, int32_t ffn, const void *g, const void *u, int64_t ld,
+                                        void *h, uint8_t *h_codes, float *h_scales, uint8_t *saved_codes,
+                                        float *saved_scales, moe_stream_t stream);
+
+/*
+ * moe_swiglu_backward_e4m3 -- the gradient of h = SiLU(g) * u from the kept
+ * codes: with g, u the values they stand for and s = sigmoid(g),
+ *
+ *   dg = dh * u * s * (1 + g * (1 - s)),   du = dh * g * s,   h = g * s * u
+ *
+ *   dh            [R, ffn] bf16
+ *   dg, du        [R, ffn] bf16 out, row pitch ld elements each
+ *   h             [R, ffn] bf16 out, or NULL (for the down projection's
+ *                 weight gradient, without having kept it)
+ *   d_codes       [R, 2 ffn], d_scales [R, 2 ffn/128] out, or both NULL: dg,
+ *                 then du of each row in blocks with MOE_SCALE_AMAX, from fp32
+ *                 (the rows of the data gradient); needs ffn % 128 == 0
+ * ffn % 16 == 0, else MOE_ERR_UNSUPPORTED.
+ */
+MOE_API moe_status moe_swiglu_backward_e4m3(int32_t R, int32_t ffn, const uint8_t *saved_codes,
+                                            const float *saved_scales, const void *dh, void *dg, void *du,
+                                            int64_t ld, void *h, uint8_t *d_codes, float *d_scales,
+                                            moe_stream_t stream);
+
+/*
+ * moe_grouped_wgrad -- the weight gradient of a grouped product.  For every
+ * expert e:
+ *
+ *   dw[e,n,k] = sum_{r of e} dy[r,n] * x[r,k]   (accumulate == 0; zeros for an
+ *                                               expert without rows)
+ *   dw[e,n,k] += the same                       (accumulate != 0)
+ * summed in fp32, rounded once to dw_dtype (and once more by the addition).
+ *
+ *   dy   [R, N] bf16, row pitch ld_dy elements
+ *   x    x_dtype MOE_BF16: [R, K], x_scales NULL; MOE_FP8_E4M3: codes [R, K]
+ *        with x_scales [R, ceil(K/128)], x = code * scale: exact when the
+ *        scales are powers of two, else rounded to bf16
+ *   dw   [E, N, K] MOE_F32 or MOE_BF16, in and out
+ * N % 16 == 0 and K % 16 == 0, else MOE_ERR_UNSUPPORTED.
+ */
+MOE_API moe_status moe_grouped_wgrad(int32_t R, int32_t N, int32_t K, int32_t E, int32_t x_dtype,
+                                     int32_t dw_dtype, int32_t accumulate, const void *dy, int64_t ld_dy,
+                                     const void *x, const float *x_scales, const int32_t *offsets, void *dw,
+                                     moe_stream_t stream);
+
+/*
+ * moe_router_losses -- load-balance and z losses of a batch's router logits.
+ * With p = softmax(logits[t,:]), lse[t] its log-sum-exp, n the tokens whose
+ * mask is nonzero (all of them when mask is NULL) and c_e the assignments of
+ * those tokens to expert e:
+ *
+ *   loss[0] = balance_coef * E * sum_e (c_e / (n k)) * (mean over them of p[t,e])
+ *   loss[1] = z_coef * mean over them of lse[t]^2          (both 0 when n == 0)
+ *
+ *   logits   [T, E] fp32      topk_idx [T, k] int32      mask [T] bytes or NULL
+ *   loss     [2] fp32 out
+ *   counts   [E+1] int32 out: c_e, then n
+ *   lse      [T] fp32 out
+ *   workspace: moe_router_losses_workspace_size() bytes
+ * A row whose logits are all -inf has no probabilities: it adds nothing to
+ * the means' sums.  Indices outside [0, E) are skipped and flag
+ * MOE_ERR_DEVICE_BOUNDS.  Bit-reproducible.
+ */
+MOE_API moe_status moe_router_losses(int32_t T, int32_t E, int32_t k, const float *logits,
+                                     const int32_t *topk_idx, const uint8_t *mask, float balance_coef,
+                                     float z_coef, float *loss, int32_t *counts, float *lse, void *workspace,
+                                     size_t workspace_bytes, moe_stream_t stream);
+MOE_API moe_status moe_router_losses_workspace_size(int32_t T, int32_t E, size_t *bytes);
+MOE_API moe_status moe_router_losses_workspace_size_for(int32_t T, int32_t E, int32_t num_sms, size_t *bytes);
+
+/*
+ * moe_router_losses_backward -- the gradient of the router's logits: of
+ * *grad_loss * (loss[0] + loss[1]) with the counts held constant (grad_loss
+ * NULL: 1), and, when topk_w [T, k] (moe_router_topk's) and its gradient
+ * d_topk_w are given, of the renormalised weights:
+ *
+ *   d_logits[t,e] = *grad_loss * mask_t / n * p[t,e] *
+ *                     (balance_coef * E * (f_e - sum_j f_j p[t,j]) + 2 z_coef lse[t])
+ *                 + (e == topk_idx[t,j]) * w_tj * (dw_tj - sum_i w_ti dw_ti)
+ * with f_e = c_e / (n k).  Masked tokens keep the second part.  A row whose
+ * logits are all -inf gets no gradient from the losses.
+ *   d_logits [T, E] fp32 out
+ */
+MOE_API moe_status moe_router_losses_backward(int32_t T, int32_t E, int32_t k, const float *logits,
+                                              const int32_t *topk_idx, const uint8_t *mask,
+                                              float balance_coef, float z_coef, const int32_t *counts,
+                                              const float *lse, const float *grad_loss, const float *topk_w,
+                                              const float *d_topk_w, float *d_logits, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -49,6 +49,7 @@ class MoEError(RuntimeError):
 _LIB = None
 _VP = ctypes.c_void_p
 _PP = ctypes.POINTER(moe_problem)
+_I, _L, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 _SIGS = {
     "moe_router_topk": [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP],
@@ -74,6 +75,15 @@ _SIGS = {
     "moe_permute_static_scratch": [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP],
     "moe_quantize_rows_e4m3": [ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP],
     "moe_split_rows_e4m3x2": [ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP],
+    "moe_quantize_blocks_e4m3": [_I] * 4 + [_VP, _L, _VP, _VP, _VP],
+    "moe_grouped_block_gemm": [_I] * 6 + [_VP] * 7,
+    "moe_swiglu_save_e4m3": [_I, _I, _VP, _VP, _L] + [_VP] * 6,
+    "moe_swiglu_backward_e4m3": [_I, _I] + [_VP] * 5 + [_L] + [_VP] * 4,
+    "moe_grouped_wgrad": [_I] * 7 + [_VP, _L] + [_VP] * 5,
+    "moe_router_losses": [_I] * 3 + [_VP] * 3 + [_F, _F] + [_VP] * 4 + [ctypes.c_size_t, _VP],
+    "moe_router_losses_workspace_size": [_I, _I, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_router_losses_workspace_size_for": [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_router_losses_backward": [_I] * 3 + [_VP] * 3 + [_F, _F] + [_VP] * 7,
 }
 STAGES = ("router", "permute", "gate_up", "down", "shared", "combine")
 EXPORTS = tuple(_SIGS)
@@ -424,3 +434,225 @@ def layer_forward(p, case, out=None, workspace=None, want_routing=False, stream=
     else:
         moe_layer_forward_timed(*args, timer, stream=stream)
     return (out, idx, w, counts) if want_routing else out
+
+
+# ---------------------------------------------------------------------------
+# training the routed experts in 8 bits
+# ---------------------------------------------------------------------------
+
+BLOCK = 128
+SCALE = {"amax": 0, "pow2": 1}
+_TYPES = {torch.float32: DTYPE["f32"], torch.bfloat16: DTYPE["bf16"]}
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _type(t, name: str) -> int:
+    if t not in _TYPES:
+        raise ValueError(f"{name}: {t}, the call takes float32 or bfloat16")
+    return _TYPES[t]
+
+
+def _exact(t: Optional[torch.Tensor], name: str, shape, dtype) -> None:
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: {t.dtype} {list(t.shape)}, the call takes {dtype} {list(shape)}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None) -> int:
+    """The row pitch in elements of a matrix whose rows may lie apart."""
+    if t.dim() != 2 or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name}: {t.dtype} {list(t.shape)}, the call takes a matrix" + (f" of {dtype}" if dtype else ""))
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: the elements of a row must be adjacent and rows must not overlap")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _pitched(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("the library takes device tensors")
+    return t.data_ptr()
+
+
+def quantize_blocks(x, scale="amax", codes=None, scales=None, stream=None):
+    """moe_quantize_blocks_e4m3 of the rows of x [..., cols] (a matrix's rows
+    may lie apart): (codes uint8 [..., cols], scales fp32 [..., blocks])."""
+    if scale not in SCALE:
+        raise ValueError(f"scale: {scale!r}, the call takes {sorted(SCALE)}")
+    kind, cols = _type(x.dtype, "x"), int(x.shape[-1])
+    m = x if x.dim() == 2 else x.reshape(-1, cols)
+    ld, sshape = _rows(m, "x"), (*x.shape[:-1], _blocks(cols))
+    codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device) if codes is None else codes
+    scales = torch.empty(sshape, dtype=torch.float32, device=x.device) if scales is None else scales
+    _exact(codes, "codes", x.shape, torch.uint8)
+    _exact(scales, "scales", sshape, torch.float32)
+    _call("moe_quantize_blocks_e4m3", m.shape[0], cols, kind, SCALE[scale], _pitched(m), ld, _ptr(codes), _ptr(scales),
+          _stream(stream))
+    return codes, scales
+
+
+def grouped_block_gemm(a, a_scales, offsets, w, w_scales, transposed=False, out_dtype=torch.bfloat16, out=None,
+                       stream=None):
+    """moe_grouped_block_gemm: rows a [R, K] (codes) of each expert times its
+    w [E, N, K] (transposed: [E, K, N]) -> [R, N]."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a: [R, K] and w: [E, N, K] are expected")
+    R, K = a.shape
+    E, N, Kw = (w.shape[0], w.shape[2], w.shape[1]) if transposed else w.shape
+    if K != Kw:
+        raise ValueError(f"w: {list(w.shape)} does not reduce over {K} columns")
+    kind = _type(out_dtype if out is None else out.dtype, "out")
+    out = torch.empty((R, N), dtype=out_dtype, device=a.device) if out is None else out
+    sshape = (E, _blocks(K), _blocks(N)) if transposed else (E, _blocks(N), _blocks(K))
+    _exact(a, "a", (R, K), torch.uint8)
+    _exact(a_scales, "a_scales", (R, _blocks(K)), torch.float32)
+    _exact(offsets, "offsets", (E + 1,), torch.int32)
+    _exact(w, "w", w.shape, torch.uint8)
+    _exact(w_scales, "w_scales", sshape, torch.float32)
+    _exact(out, "out", (R, N), out.dtype)
+    _call("moe_grouped_block_gemm", R, K, N, E, int(bool(transposed)), kind, _ptr(a), _ptr(a_scales), _ptr(offsets),
+          _ptr(w), _ptr(w_scales), _ptr(out), _stream(stream))
+    return out
+
+
+class SwigluSaved(NamedTuple):
+    """What swiglu_save returns: h (bf16) and its codes and scales where asked
+    for, and g and u as kept for the backward pass."""
+    h: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    saved: torch.Tensor
+    saved_scales: torch.Tensor
+
+
+class SwigluGrads(NamedTuple):
+    """What swiglu_backward returns: dg | du [R, 2 ffn], h again and the codes
+    and scales of dg | du where asked for."""
+    d_gu: torch.Tensor
+    h: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+
+
+def swiglu_save(g, u, want_h=False, want_codes=True, stream=None) -> SwigluSaved:
+    """moe_swiglu_save_e4m3 of g and u [R, ffn] bf16 (for instance the halves
+    of one product's rows)."""
+    ld = _rows(g, "g", torch.bfloat16)
+    if _rows(u, "u", torch.bfloat16) != ld or u.shape != g.shape:
+        raise ValueError("g and u: two matrices of one shape and row pitch are expected")
+    R, f = g.shape
+
+    def new(*shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=g.device)
+
+    h = new(R, f, dtype=torch.bfloat16) if want_h else None
+    codes = new(R, f, dtype=torch.uint8) if want_codes else None
+    scales = new(R, _blocks(f), dtype=torch.float32) if want_codes else None
+    saved, saved_scales = new(2, R, f, dtype=torch.uint8), new(2, R, _blocks(f), dtype=torch.float32)
+    _call("moe_swiglu_save_e4m3", R, f, _pitched(g), _pitched(u), ld, _ptr(h), _ptr(codes), _ptr(scales), _ptr(saved),
+          _ptr(saved_scales), _stream(stream))
+    return SwigluSaved(h, codes, scales, saved, saved_scales)
+
+
+def swiglu_backward(saved, saved_scales, dh, want_h=False, want_codes=False, stream=None) -> SwigluGrads:
+    """moe_swiglu_backward_e4m3 of what swiglu_save kept and dh [R, ffn] bf16."""
+    if dh.dim() != 2:
+        raise ValueError("dh: [R, ffn] is expected")
+    R, f = dh.shape
+    _exact(dh, "dh", (R, f), torch.bfloat16)
+    _exact(saved, "saved", (2, R, f), torch.uint8)
+    _exact(saved_scales, "saved_scales", (2, R, _blocks(f)), torch.float32)
+    d_gu = torch.empty((R, 2 * f), dtype=torch.bfloat16, device=dh.device)
+    h = torch.empty((R, f), dtype=torch.bfloat16, device=dh.device) if want_h else None
+    codes = torch.empty((R, 2 * f), dtype=torch.uint8, device=dh.device) if want_codes else None
+    scales = torch.empty((R, _blocks(2 * f)), dtype=torch.float32, device=dh.device) if want_codes else None
+    dg = _ptr(d_gu)
+    _call("moe_swiglu_backward_e4m3", R, f, _ptr(saved), _ptr(saved_scales), _ptr(dh), dg,
+          dg + 2 * f if dg else None, 2 * f, _ptr(h), _ptr(codes), _ptr(scales), _stream(stream))
+    return SwigluGrads(d_gu, h, codes, scales)
+
+
+def grouped_wgrad(dy, x, x_scales, offsets, dw=None, accumulate=False, dw_dtype=torch.float32, stream=None):
+    """moe_grouped_wgrad: dw [E, N, K] of dy [R, N] bf16 (its rows may lie
+    apart) and x [R, K], bf16 (x_scales None) or codes with their scales."""
+    ld = _rows(dy, "dy", torch.bfloat16)
+    R, N = dy.shape
+    K, E = x.shape[-1], offsets.numel() - 1
+    _exact(x, "x", (R, K), torch.bfloat16 if x_scales is None else torch.uint8)
+    _exact(x_scales, "x_scales", (R, _blocks(K)), torch.float32)
+    _exact(offsets, "offsets", (E + 1,), torch.int32)
+    if dw is None:
+        if accumulate:
+            raise ValueError("dw: accumulating needs the tensor to add to")
+        dw = torch.empty((E, N, K), dtype=dw_dtype, device=dy.device)
+    kind = _type(dw.dtype, "dw")
+    _exact(dw, "dw", (E, N, K), dw.dtype)
+    _call("moe_grouped_wgrad", R, N, K, E, DTYPE["bf16" if x_scales is None else "fp8"], kind, int(bool(accumulate)),
+          _pitched(dy), ld, _ptr(x), _ptr(x_scales), _ptr(offsets), _ptr(dw), _stream(stream))
+    return dw
+
+
+class RouterLosses(NamedTuple):
+    """What router_losses returns: loss [2] (balance, z), counts [E + 1] (the
+    experts', then the unmasked tokens), lse [T], and the coefficients."""
+    loss: torch.Tensor
+    counts: torch.Tensor
+    lse: torch.Tensor
+    balance: float
+    z: float
+
+
+def moe_router_losses_workspace_size(T: int, E: int) -> int:
+    n = ctypes.c_size_t(0)
+    _call("moe_router_losses_workspace_size", T, E, ctypes.byref(n))
+    return int(n.value)
+
+
+def moe_router_losses_workspace_size_for(T: int, E: int, num_sms: int) -> int:
+    n = ctypes.c_size_t(0)
+    _call("moe_router_losses_workspace_size_for", T, E, num_sms, ctypes.byref(n))
+    return int(n.value)
+
+
+def _check_router(logits, idx, mask):
+    if logits.dim() != 2 or idx.dim() != 2:
+        raise ValueError("logits: [T, E] and topk_idx: [T, k] are expected")
+    T, E = logits.shape
+    k = idx.shape[1]
+    _exact(logits, "logits", (T, E), torch.float32)
+    _exact(idx, "topk_idx", (T, k), torch.int32)
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (T,)):
+        raise ValueError(f"mask: {mask.dtype} {list(mask.shape)}, the call takes bool or uint8 [{T}]")
+    return T, E, k
+
+
+def router_losses(logits, topk_idx, balance, z, mask=None, workspace=None, stream=None) -> RouterLosses:
+    """moe_router_losses of logits [T, E] and the chosen experts [T, k]."""
+    T, E, k = _check_router(logits, topk_idx, mask)
+    dev = logits.device
+    loss = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(moe_router_losses_workspace_size(T, E), dtype=torch.uint8, device=dev)
+    _call("moe_router_losses", T, E, k, _ptr(logits), _ptr(topk_idx), _ptr(mask), balance, z, _ptr(loss), _ptr(counts),
+          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    return RouterLosses(loss, counts, lse, balance, z)
+
+
+def router_losses_backward(logits, topk_idx, losses: RouterLosses, grad=None, topk_w=None, d_topk_w=None, mask=None,
+                           stream=None):
+    """moe_router_losses_backward: the gradient of the logits [T, E]; grad is
+    a device scalar (None: 1)."""
+    T, E, k = _check_router(logits, topk_idx, mask)
+    _exact(losses.counts, "counts", (E + 1,), torch.int32)
+    _exact(losses.lse, "lse", (T,), torch.float32)
+    _check(grad, "grad", 1, 4, torch.float32)
+    _exact(topk_w, "topk_w", (T, k), torch.float32)
+    _exact(d_topk_w, "d_topk_w", (T, k), torch.float32)
+    d_logits = torch.empty_like(logits)
+    _call("moe_router_losses_backward", T, E, k, _ptr(logits), _ptr(topk_idx), _ptr(mask), losses.balance, losses.z,
+          _ptr(losses.counts), _ptr(losses.lse), _ptr(grad), _ptr(topk_w), _ptr(d_topk_w), _ptr(d_logits),
+          _stream(stream))
+    return d_logits

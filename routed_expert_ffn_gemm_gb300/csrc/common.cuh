@@ -71,6 +71,13 @@ moe_status make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint6
 moe_status make_tmap_kpair(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            int elem_bytes, uint32_t box_rows);
 
+// 3-D row-major map [outer, rows, cols] with row pitch `pitch` bytes and
+// `rows` rows per outer index; elements of 1 byte, 2 (bf16) or 4 (fp32); box
+// {box_cols, box_rows, 1}, swizzle as above, zero fill out of bounds in every
+// dimension (stores are clipped there).
+moe_status make_tmap_3d(CUtensorMap* map, const void* base, uint64_t outer, uint64_t rows, uint64_t cols,
+                        uint64_t pitch, int elem_bytes, uint32_t box_rows, uint32_t box_cols, int swizzle_bytes);
+
 // ---------------------------------------------------------------------------
 // launches: programmatic dependent launch
 // ---------------------------------------------------------------------------

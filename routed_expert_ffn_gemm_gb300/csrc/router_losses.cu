@@ -1,0 +1,362 @@
+// The router's balance loss and z loss with the per-expert counts, and the
+// gradient of the logits.
+//
+//   p = softmax(l[t,:]), f_e = counts_e / (n k), P_e = mean of p[t,e] over
+//   the n unmasked tokens;  balance = alpha E sum_e f_e P_e,
+//   z = beta mean lse_t^2.  f holds counts and has no gradient, so
+//   dl[t,e] = (alpha E / n) p (f_e - sum_j f_j p_j) + (2 beta / n) lse p,
+//   plus the gradient through the kept weights (a softmax over the kept
+//   slots): w_j (dw_j - sum_i w_i dw_i) at expert idx[t,j].
+//
+// Both directions read the logits once, a row by a group of LG lanes that
+// keep it in registers; they are bound by that read (and the gradient's
+// write), or by launch latency when there are few tokens.  Sums over tokens
+// go lane -> warp -> CTA -> fixed-order sum over CTAs: no floating-point
+// atomics, so every run gives the same bits.
+#include <math.h>
+
+#include "train.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Lanes LG hold a row: lane l has columns (i * LG + l) * VEC + c.
+template <int LG, int VEC, int NI>
+struct Row {
+  float v[NI * VEC];
+  __device__ __forceinline__ static int col(int i, int l) { return (i * LG + l) * VEC; }
+  __device__ __forceinline__ void load(const float* row, int E, int l) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e = col(i, l);
+      if constexpr (VEC == 4) {
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e < E) q = __ldg(reinterpret_cast<const float4*>(row + e));
+        v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+      } else {
+        v[i] = e < E ? __ldg(row + e) : -INFINITY;
+      }
+    }
+  }
+};
+
+template <int LG>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// (fmaxf drops NaN: a NaN logit shows in the sum of exponentials instead)
+template <int LG>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = LG / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Workspace of one CTA: prob sums [E] (float), counts [E] (int), sum of
+// lse^2 (float), unmasked tokens (int).
+__host__ __device__ inline size_t part_words(int E) { return 2 * (size_t)E + 2; }
+
+// Sums the CTAs' parts in CTA order and writes counts and losses.  One CTA.
+__device__ void finalize(const RouterLossArgs& a, const uint32_t* parts, int nparts) {
+  __shared__ float red_p[kThreads], red_z[kWarps];
+  __shared__ int red_n[kWarps];
+  const size_t pw = part_words(a.E);
+  float zs = 0.f;
+  int n = 0;
+  for (int b = threadIdx.x; b < nparts; b += kThreads) {
+    zs += __uint_as_float(__ldcg(parts + b * pw + 2 * a.E));
+    n += (int)__ldcg(parts + b * pw + 2 * a.E + 1);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    zs += __shfl_xor_sync(0xffffffffu, zs, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    red_z[threadIdx.x >> 5] = zs;
+    red_n[threadIdx.x >> 5] = n;
+  }
+  __syncthreads();
+  zs = 0.f;
+  n = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    zs += red_z[w];
+    n += red_n[w];
+  }
+  float dot = 0.f;  // sum over this thread's experts of counts_e * P_e
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    float P = 0.f;
+    int c = 0;
+    for (int b = 0; b < nparts; ++b) {
+      P += __uint_as_float(__ldcg(parts + b * pw + e));
+      c += (int)__ldcg(parts + b * pw + a.E + e);
+    }
+    a.counts[e] = c;
+    dot += (float)c * P;
+  }
+  red_p[threadIdx.x] = dot;
+  __syncthreads();
+  for (int o = kThreads / 2; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) red_p[threadIdx.x] += red_p[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const float fn = (float)n;
+    a.counts[a.E] = n;
+    a.loss[0] = n > 0 ? a.balance * (float)a.E * (red_p[0] / (fn * (float)a.k)) / fn : 0.f;
+    a.loss[1] = n > 0 ? a.z * (zs / fn) : 0.f;
+  }
+}
+
+template <int LG, int VEC, int NI>
+__global__ void __launch_bounds__(kThreads) router_losses_kernel(const RouterLossArgs a) {
+  griddep_begin();
+  extern __shared__ uint32_t sm[];
+  float* psum = reinterpret_cast<float*>(sm);                 // [kWarps][E]
+  int* hist = reinterpret_cast<int*>(sm + kWarps * a.E);      // [E]
+  __shared__ float red_z[kWarps];
+  __shared__ int red_n[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (LG - 1);
+  constexpr int RPW = 32 / LG;  // rows of a warp at a time
+  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  float P[NI * VEC], zs = 0.f;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NI * VEC; ++i) P[i] = 0.f;
+  const int step = gridDim.x * kWarps * RPW;
+  for (int t0 = (blockIdx.x * kWarps + warp) * RPW; t0 < a.T; t0 += step) {
+    const int t = t0 + lane / LG;
+    const bool here = t < a.T, live = here && (a.mask == nullptr || a.mask[t] != 0);
+    Row<LG, VEC, NI> r;
+    if (here) r.load(a.logits + (size_t)t * a.E, a.E, l);
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NI * VEC; ++i) {
+      if (!here) r.v[i] = -INFINITY;
+      m = fmaxf(m, r.v[i]);
+    }
+    m = group_max<LG>(m);
+    const float m0 = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI * VEC; ++i) {
+      r.v[i] = __expf(r.v[i] - m0);
+      sum += r.v[i];
+    }
+    sum = group_sum<LG>(sum);
+    // a row without any logit above -inf has no probabilities: it adds
+    // nothing to P and z, and its lse of -inf gives it no gradient
+    const float lse = sum == 0.f ? -INFINITY : m0 + logf(sum), inv = live && sum != 0.f ? 1.f / sum : 0.f;
+    if (here && l == 0) a.lse[t] = lse;
+    if (live && sum != 0.f) {
+#pragma unroll
+      for (int i = 0; i < NI * VEC; ++i) P[i] = fmaf(r.v[i], inv, P[i]);
+      if (l == 0) zs = fmaf(lse, lse, zs);
+    }
+    if (live && l == 0) ++n;
+    if (live)
+      for (int j = l; j < a.k; j += LG) {
+        const int e = a.idx[(size_t)t * a.k + j];
+        if (e >= 0 && e < a.E)
+          atomicAdd(hist + e, 1);
+        else
+          set_device_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    zs += __shfl_xor_sync(0xffffffffu, zs, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+#pragma unroll
+  for (int i = 0; i < NI * VEC; ++i) {
+#pragma unroll
+    for (int o = 16; o >= LG; o >>= 1) P[i] += __shfl_xor_sync(0xffffffffu, P[i], o);
+    const int e = Row<LG, VEC, NI>::col(i / VEC, l) + i % VEC;
+    if (lane < LG && e < a.E) psum[warp * a.E + e] = P[i];
+  }
+  if (lane == 0) {
+    red_z[warp] = zs;
+    red_n[warp] = n;
+  }
+  __syncthreads();
+  uint32_t* part = static_cast<uint32_t*>(a.workspace) + blockIdx.x * part_words(a.E);
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    float s = 0.f;
+    for (int w = 0; w < kWarps; ++w) s += psum[w * a.E + e];
+    part[e] = __float_as_uint(s);
+    part[a.E + e] = (uint32_t)hist[e];
+  }
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+    int c = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      s += red_z[w];
+      c += red_n[w];
+    }
+    part[2 * a.E] = __float_as_uint(s);
+    part[2 * a.E + 1] = (uint32_t)c;
+  }
+  if (gridDim.x == 1) {
+    __syncthreads();
+    finalize(a, part, 1);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) router_losses_finalize_kernel(const RouterLossArgs a, int nparts) {
+  griddep_begin();
+  finalize(a, static_cast<const uint32_t*>(a.workspace), nparts);
+}
+
+template <int LG, int VEC, int NI>
+__global__ void __launch_bounds__(kThreads) router_losses_backward_kernel(const RouterLossGradArgs a) {
+  griddep_begin();
+  extern __shared__ uint32_t sm[];
+  float* f = reinterpret_cast<float*>(sm);                    // [E] counts / (n k)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (LG - 1);
+  constexpr int RPW = 32 / LG;
+  // what the kept weights add, at their experts' columns: one row per group
+  float* add = f + a.E + (warp * RPW + lane / LG) * a.E;
+  const int n = a.counts[a.E];
+  const float inv_n = n > 0 ? 1.f / (float)n : 0.f, inv_nk = inv_n / (float)a.k;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) f[e] = (float)a.counts[e] * inv_nk;
+  if (a.w != nullptr)
+    for (int e = l; e < a.E; e += LG) add[e] = 0.f;
+  __syncthreads();
+  const float up = (a.grad != nullptr ? *a.grad : 1.f) * inv_n;
+  const float cb = a.balance * (float)a.E, cz = 2.f * a.z;
+  const int step = gridDim.x * kWarps * RPW;
+  for (int t0 = (blockIdx.x * kWarps + warp) * RPW; t0 < a.T; t0 += step) {
+    const int t = t0 + lane / LG;
+    const bool here = t < a.T, live = here && (a.mask == nullptr || a.mask[t] != 0);
+    Row<LG, VEC, NI> r;
+    float lse = -INFINITY;
+    if (here) {
+      r.load(a.logits + (size_t)t * a.E, a.E, l);
+      lse = a.lse[t];
+    }
+    if (a.w != nullptr) {
+      float dot = 0.f;
+      if (here)
+        for (int j = l; j < a.k; j += LG) dot = fmaf(a.w[(size_t)t * a.k + j], a.dw[(size_t)t * a.k + j], dot);
+      dot = group_sum<LG>(dot);
+      if (here)
+        for (int j = l; j < a.k; j += LG) {
+          const size_t at = (size_t)t * a.k + j;
+          const int e = a.idx[at];
+          if (e >= 0 && e < a.E)
+            atomicAdd(add + e, a.w[at] * (a.dw[at] - dot));  // (distinct experts: one add each)
+          else
+            set_device_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+        }
+      __syncwarp();
+    }
+    const bool some = live && lse != -INFINITY;
+    float fp = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI * VEC; ++i) {
+      const int e = Row<LG, VEC, NI>::col(i / VEC, l) + i % VEC;
+      r.v[i] = some ? __expf(r.v[i] - lse) : 0.f;
+      if (e < a.E) fp = fmaf(f[e], r.v[i], fp);
+    }
+    fp = group_sum<LG>(fp);
+    const float zt = some ? cz * lse : 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e0 = Row<LG, VEC, NI>::col(i, l);
+      if (!here || e0 >= a.E) continue;
+      float d[VEC];
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        d[c] = some ? up * (r.v[i * VEC + c] * fmaf(cb, f[e0 + c] - fp, zt)) : 0.f;
+        if (a.w != nullptr) d[c] += add[e0 + c];
+      }
+      float* to = a.dlogits + (size_t)t * a.E + e0;
+      if constexpr (VEC == 4)
+        *reinterpret_cast<float4*>(to) = make_float4(d[0], d[1], d[2], d[3]);
+      else
+        *to = d[0];
+    }
+    if (a.w != nullptr) {
+      __syncwarp();
+      if (here)
+        for (int j = l; j < a.k; j += LG) {
+          const int e = a.idx[(size_t)t * a.k + j];
+          if (e >= 0 && e < a.E) add[e] = 0.f;
+        }
+      __syncwarp();
+    }
+  }
+}
+
+// One of the row layouts: vectors of four when the rows are 16-byte aligned
+// (E % 4 == 0), fewer lanes a row when it is short.
+template <template <int, int, int> class Launch, typename Args>
+moe_status dispatch(int E, const Args& a, int blocks, cudaStream_t s) {
+  if (E % 4 == 0) {
+    if (E <= 32) return Launch<8, 4, 1>::run(a, blocks, s);
+    if (E <= 64) return Launch<16, 4, 1>::run(a, blocks, s);
+    if (E <= 128) return Launch<32, 4, 1>::run(a, blocks, s);
+    if (E <= 256) return Launch<32, 4, 2>::run(a, blocks, s);
+    if (E <= 512) return Launch<32, 4, 4>::run(a, blocks, s);
+    return Launch<32, 4, 8>::run(a, blocks, s);
+  }
+  if (E <= 32) return Launch<8, 1, 4>::run(a, blocks, s);
+  if (E <= 128) return Launch<32, 1, 4>::run(a, blocks, s);
+  if (E <= 512) return Launch<32, 1, 16>::run(a, blocks, s);
+  return Launch<32, 1, 32>::run(a, blocks, s);
+}
+// Rows a CTA holds at a time under dispatch()'s layouts.
+int rows_per_pass(int E) {
+  const int lg = E <= 32 ? 8 : E % 4 == 0 && E <= 64 ? 16 : 32;
+  return kThreads / lg;
+}
+
+template <int LG, int VEC, int NI>
+struct Forward {
+  static moe_status run(const RouterLossArgs& a, int blocks, cudaStream_t s) {
+    const size_t smem = 4 * (size_t)(kWarps + 1) * a.E;
+    MOE_TRY_CUDA(launch_k(router_losses_kernel<LG, VEC, NI>, dim3(blocks), dim3(kThreads), smem, s, a));
+    return MOE_OK;
+  }
+};
+template <int LG, int VEC, int NI>
+struct Backward {
+  static moe_status run(const RouterLossGradArgs& a, int blocks, cudaStream_t s) {
+    const size_t smem = 4 * (size_t)(1 + (a.w != nullptr ? kThreads / LG : 0)) * a.E;
+    MOE_TRY_CUDA(launch_k(router_losses_backward_kernel<LG, VEC, NI>, dim3(blocks), dim3(kThreads), smem, s, a));
+    return MOE_OK;
+  }
+};
+
+int forward_blocks(int T, int E, int num_sms) {
+  const int want = ceil_div(T, rows_per_pass(E));
+  return want < num_sms ? want : num_sms;
+}
+
+}  // namespace
+
+size_t router_losses_workspace(int T, int E, int num_sms) {
+  return 4 * part_words(E) * (size_t)forward_blocks(T > 0 ? T : 1, E, num_sms);
+}
+
+moe_status router_losses_launch(const RouterLossArgs& a, cudaStream_t s) {
+  const int blocks = forward_blocks(a.T > 0 ? a.T : 1, a.E, a.num_sms);
+  MOE_TRY((dispatch<Forward, RouterLossArgs>(a.E, a, blocks, s)));
+  if (blocks > 1)
+    MOE_TRY_CUDA(launch_k(router_losses_finalize_kernel, dim3(1), dim3(kThreads), 0, s, a, blocks));
+  return MOE_OK;
+}
+
+moe_status router_losses_backward_launch(const RouterLossGradArgs& a, cudaStream_t s) {
+  const int want = ceil_div(a.T, rows_per_pass(a.E)), most = 4 * a.num_sms;
+  return dispatch<Backward, RouterLossGradArgs>(a.E, a, want < most ? want : most, s);
+}
+
+}  // namespace moe
