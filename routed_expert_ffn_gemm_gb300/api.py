@@ -196,8 +196,11 @@ def _check_layer(p, *tensors):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    # (torch.cuda.current_stream() builds a Stream object: 10 us of host time
+    # a call where a decode step's kernels take 5)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _call(name, *args):
@@ -456,7 +459,7 @@ def _type(t, name: str) -> int:
 
 
 def _exact(t: Optional[torch.Tensor], name: str, shape, dtype) -> None:
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+    if t is not None and (t.dtype is not dtype or t.shape != shape):
         raise ValueError(f"{name}: {t.dtype} {list(t.shape)}, the call takes {dtype} {list(shape)}")
 
 
@@ -603,6 +606,11 @@ class RouterLosses(NamedTuple):
     z: float
 
 
+@functools.lru_cache(maxsize=256)
+def _router_workspace(T: int, E: int, device: int) -> int:
+    return moe_router_losses_workspace_size(T, E)
+
+
 def moe_router_losses_workspace_size(T: int, E: int) -> int:
     n = ctypes.c_size_t(0)
     _call("moe_router_losses_workspace_size", T, E, ctypes.byref(n))
@@ -635,7 +643,7 @@ def router_losses(logits, topk_idx, balance, z, mask=None, workspace=None, strea
     counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
     lse = torch.empty(T, dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(moe_router_losses_workspace_size(T, E), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_router_workspace(T, E, torch._C._cuda_getDevice()), dtype=torch.uint8, device=dev)
     _call("moe_router_losses", T, E, k, _ptr(logits), _ptr(topk_idx), _ptr(mask), balance, z, _ptr(loss), _ptr(counts),
           _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     return RouterLosses(loss, counts, lse, balance, z)

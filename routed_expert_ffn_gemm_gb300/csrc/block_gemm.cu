@@ -8,20 +8,26 @@
 // block's sum leaves tensor memory before the next one's scale applies and
 // is added in fp32 registers: acc += (sa sw) * D.
 //
-// Orientation: the MMA's M side is output channels (weights are always full
-// tiles), its N side rows, so that a few rows cost few columns.  A unit is
-// 256 channels x up to 256 rows of one expert on a pair of CTAs (cta_group::2:
-// each CTA stages its 128 channels and half of the rows, 32 KB a block, which
-// halves the row bytes per SM; at one CTA per tile the 8-bit rate asks L2 for
-// more than it gives).  A group's rows are cut into equal tiles of at most
-// 256; each unit's rows come by the smallest of four copy boxes that holds
-// them.  Units run row tiles first inside bands of 16, so that a weight tile
-// is read from memory once while the band's rows stay in L2.
+// A unit is 256 channels x up to 256 rows of one expert on a cluster of two
+// CTAs.  With many rows the CTAs split the rows, 128 on the MMA's M side each,
+// and share the weights (N side); an accumulator lane is then a row, whose
+// scale is one value for all of a lane's columns.  With few rows they split
+// the channels (M side) and share the rows (N side, a multiple of 32), so
+// that few rows cost few columns; the scales then come per column.  Each CTA
+// loads half of what both share and multicasts it, so that L2 gives every
+// byte once a cluster.  The MMAs are each CTA's own (cta_group::1): a block's
+// sum goes from the tensor cores to the registers and the buffer back within
+// the CTA; with one MMA for both CTAs that round trip crosses them and bounds
+// the loop.
+// Units run row tiles first inside bands of 16, so that a weight tile is read
+// from memory once while the band's rows stay in L2.
 //
-// Roles: warp 0 copies (TMA), warp 1 issues the MMAs, warp 2 prepares
-// sa * sw of each block in shared memory, warps 4..11 hold the accumulators:
-// each warp has 32 channels and alternate chunks of 32 rows.  Two
-// accumulator buffers in tensor memory: one fills while the other is read.
+// Roles: warp 0 copies (TMA), warp 1 issues the MMAs, warp 2 brings the
+// scales to shared memory (cp.async), warps 4..11 hold the accumulators:
+// a quarter of the lanes each, alternate chunks of 32 columns.  Tensor memory
+// holds two buffers of 256 columns, one filling while the other is read: one
+// block's sums with rows on M, two or four blocks' side by side with rows on N
+// (a hand-over costs some 500 cycles whatever it hands over).
 //
 // Transposed weights ([E, K, N]: the data gradient with the forward's
 // arrays) are the same tiles read MN-major by the MMA.
@@ -35,19 +41,26 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kBN = 256;                      // most rows of a unit
-constexpr int kStages = 5;
-constexpr int kABytes = 128 * 128, kBBytes = 128 * 128, kStageBytes = kABytes + kBBytes;
-constexpr int kScaleSlots = 8;
+constexpr int kStages = 4;                    // slots; block j of a step of four takes slot j
+constexpr int kOwnBytes = 128 * 128;          // the CTA's own operand (M side): 128 rows of 128 codes
+constexpr int kStageBytes = kOwnBytes + 256 * 128;  // and the shared one (N side)
+constexpr int kGroup = 4, kScaleRing = 2;  // blocks of a step: slot j holds block j; scale groups in flight
 constexpr int kEpiWarps = 8;
 constexpr int kBand = 16;                     // row tiles that share a pass over the weights
-constexpr int kOutPitch = 80;                 // bytes of a staged row of 32 channels (64), padded against conflicts
-constexpr int kOutBytes = 32 * kOutPitch;     // per warp: 32 rows
+constexpr int kChunks = 4;                    // chunks of 32 rows of an accumulating warp
+constexpr int kOutPitch = 36;                 // words of a staged pair of rows (32 channels), padded against conflicts
+// From this many rows on a unit's rows are the MMA's M side (always 256 of
+// them), below it the N side (a multiple of 32): see the head of the file.
+constexpr int kRowsOnM = 97;
+constexpr int kOutBytes = 2048;               // staging of an accumulating warp: 32 rows of 64 bytes
+static_assert(8 * 4 * kOutPitch <= kOutBytes, "staged pairs of rows");
 constexpr int kMaxGroups = 1024;
 constexpr int kOutOff = kStages * kStageBytes;
 constexpr int kScaleOff = kOutOff + kEpiWarps * kOutBytes;
-constexpr int kBarOff = kScaleOff + kScaleSlots * kBN * 4;
-// full[S], empty[S], acc_full[2], acc_empty[2], scale_full[8], scale_empty[8], drain
-constexpr int kNumBars = 2 * kStages + 4 + 2 * kScaleSlots + 1;
+constexpr int kWScaleOff = kScaleOff + kScaleRing * kGroup * kBN * 4;  // [ring][group][channel half]
+constexpr int kBarOff = kWScaleOff + kScaleRing * kGroup * 8;
+// full[S], empty[S], acc_full[2], acc_empty[2], scale_full[2], scale_empty[2], drain
+constexpr int kNumBars = 2 * kStages + 4 + 2 * kScaleRing + 1;
 constexpr int kSlotOff = kBarOff + 8 * kNumBars;
 constexpr int kAbortOff = kSlotOff + 8;
 constexpr int kOffsOff = kAbortOff + 8;
@@ -58,7 +71,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(2 * (kSmemBytes + 1024) > 232448 + 1024, "one CTA per SM");
 // Registers: 384 x 168 at launch; the accumulating warps take what the
 // other warpgroup gives back.
-constexpr int kRegsLow = 80, kRegsHigh = 208;
+constexpr int kRegsLow = 72, kRegsHigh = 216;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split");
 
 struct Params {
@@ -75,10 +88,13 @@ struct Params {
 struct Maps {
   CUtensorMap w;
   CUtensorMap a[4];  // boxes of 16, 32, 64, 128 rows
+  CUtensorMap out;   // 32 rows of 64 bytes
 };
 
 struct Unit {
   int g, row0, n_valid, n_mma, mt, tiles;
+  int batch;  // blocks whose sums share an accumulator buffer, 256 / batch columns each
+  bool rows_m;
 };
 
 __device__ __forceinline__ Unit unit_of(int u, const int* offs, const int* prefix, int E, int MT) {
@@ -96,18 +112,186 @@ __device__ __forceinline__ Unit unit_of(int u, const int* offs, const int* prefi
   const int wide = min(kBand, x.tiles - band * kBand);
   x.mt = rem / wide;
   const int rt = band * kBand + rem % wide;
-  const int cnt = offs[lo + 1] - offs[lo];
-  // equal tiles, multiples of 32 rows (the pair splits them in halves of 16)
-  const int per = ((cnt + x.tiles - 1) / x.tiles + 31) / 32 * 32;
-  x.row0 = offs[lo] + rt * per;
-  x.n_valid = min(per, cnt - rt * per);
-  x.n_mma = (x.n_valid + 31) / 32 * 32;
+  const int r0 = rt * kBN;
+  x.row0 = offs[lo] + r0;
+  x.n_valid = min(kBN, offs[lo + 1] - x.row0);
+  x.rows_m = x.n_valid >= kRowsOnM;
+  x.n_mma = x.rows_m ? kBN : (x.n_valid + 31) / 32 * 32;  // (two boxes of at least 16)
+  x.batch = x.rows_m ? 1 : x.n_mma <= 64 ? 4 : 2;
   return x;
 }
 
 // All lanes of the warp wait; the warp agrees on the outcome.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t deadline, volatile int* abort) {
   return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, deadline, abort)) != 0;
+}
+
+// Adds one accumulator buffer to a warp's registers, acc += scale * D.  The
+// warp's pieces of the buffer are 32 columns at 64 t + first; once the last
+// has arrived `release` hands the buffer back.  (Scalar adds: the registers that tcgen05.ld fills
+// would have to be moved into pairs for packed ones.)
+struct Accumulate {
+  uint32_t at;  // tensor memory: the warp's lanes, its first column
+  int first;    // its first column in the buffer
+  int row;      // this lane's row of the CTA's 128 (rows on M)
+
+  // Rows on M: one block, its scale f0 for channels 0..127, f1 for the rest.
+  template <typename Release>
+  __device__ __forceinline__ void rows_m(float (&acc)[kChunks][32], uint32_t buf, float f0, float f1,
+                                         Release release) const {
+    uint32_t d[2][16];
+    const uint32_t from = at + 256u * buf;
+    ptx::tmem_ld16(from, d[0]);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      ptx::tmem_ld_wait(d[t & 1]);
+      if (t < 7)
+        ptx::tmem_ld16(from + 64u * ((t + 1) >> 1) + 16u * ((t + 1) & 1), d[(t + 1) & 1]);
+      else
+        release();
+      const float f = t < 4 ? f0 : f1;
+      float* a = acc[t >> 1] + 16 * (t & 1);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) a[j] = fmaf(__uint_as_float(d[t & 1][j]), f, a[j]);
+    }
+  }
+
+  // Rows on N: n of BATCH blocks of 256 / BATCH columns; a column's scale is
+  // its row's times the block's for the CTA's channels.
+  template <int BATCH>
+  __device__ __forceinline__ void rows_n(float (&acc)[kChunks][32], uint32_t buf, int n, int n_mma, const float* sc,
+                                         const float* ws) const {
+    constexpr int PER = 4 / BATCH;  // chunks of this warp in a block
+    auto live = [&](int t) { return t / PER < n && (t % PER) * 64 + first < n_mma; };
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (live(t)) {
+        uint32_t d[32];
+        ptx::tmem_ld32(at + 256u * buf + 64u * t, d);
+        ptx::tmem_ld_wait(d);
+        const float w = ws[2 * (t / PER)];
+        const float* s = sc + (t / PER) * kBN + (t % PER) * 64 + first;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(s + j);
+          float* a = acc[t % PER] + j;
+          a[0] = fmaf(__uint_as_float(d[j]), s4.x * w, a[0]);
+          a[1] = fmaf(__uint_as_float(d[j + 1]), s4.y * w, a[1]);
+          a[2] = fmaf(__uint_as_float(d[j + 2]), s4.z * w, a[2]);
+          a[3] = fmaf(__uint_as_float(d[j + 3]), s4.w * w, a[3]);
+        }
+      }
+    }
+  }
+};
+
+// One warp's accumulators to memory.  Both ways go through the warp's piece
+// of shared memory, so that neighbouring lanes store 16 bytes each of one
+// row; fp32 results of rows on N are 128-byte rows as they lie.
+
+// Rows on N: the lane's channel is ch0 + lane, acc[i][j] row c0 + 64 i + j of
+// the unit.
+__device__ __forceinline__ void store_rows_n(const Params& p, const Unit& x, const float (&acc)[kChunks][32],
+                                             int ch0, int c_first, uint8_t* outb) {
+  const int lane = threadIdx.x & 31;
+  if (ch0 >= p.N) return;
+  if (lane == 0) ptx::bulk_wait_read<0>();  // (a store of rows on M)
+  __syncwarp();
+  uint32_t* st = reinterpret_cast<uint32_t*>(outb);
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c0 = c_first + 64 * i;
+    if (c0 >= x.n_valid) return;
+    if (p.out_f32) {
+      float* out = static_cast<float*>(p.out) + (size_t)(x.row0 + c0) * p.N + ch0 + lane;
+      if (ch0 + lane < p.N)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c0 + j < x.n_valid) out[(size_t)j * p.N] = acc[i][j];
+      continue;
+    }
+    const int ch = ch0 + (lane & 3) * 8;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (size_t)(x.row0 + c0) * p.N + ch;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // 16 rows: words (pair of rows, channel) in, 8 channels of two rows out
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(acc[i][16 * k + 2 * j], acc[i][16 * k + 2 * j + 1]);
+        st[j * kOutPitch + lane] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      __syncwarp();
+      const uint32_t* src = st + (lane >> 2) * kOutPitch + (lane & 3) * 8;
+      const uint4 a = *reinterpret_cast<const uint4*>(src), b = *reinterpret_cast<const uint4*>(src + 4);
+      const int c = 16 * k + 2 * (lane >> 2);
+      if (ch < p.N && c0 + c < x.n_valid)
+        *reinterpret_cast<uint4*>(out + (size_t)c * p.N) =
+            make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410), __byte_perm(b.x, b.y, 0x5410),
+                       __byte_perm(b.z, b.w, 0x5410));
+      if (ch < p.N && c0 + c + 1 < x.n_valid)
+        *reinterpret_cast<uint4*>(out + (size_t)(c + 1) * p.N) =
+            make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632), __byte_perm(b.x, b.y, 0x7632),
+                       __byte_perm(b.z, b.w, 0x7632));
+      __syncwarp();
+    }
+  }
+}
+
+// Rows on M: the lane's row is r0 + lane of the unit, acc[i][j] channel
+// ch0 + 64 i + j.  64 bytes of each row at a time: by a TMA store when all 32
+// rows are the unit's (it clips the channels past N), else row by row.
+// 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3), as the store's 64-byte
+// swizzle has it.
+__device__ __forceinline__ void store_rows_m(const Params& p, const CUtensorMap* map, const Unit& x,
+                                             const float (&acc)[kChunks][32], int r0, int ch0, uint8_t* outb) {
+  const int lane = threadIdx.x & 31;
+  if (r0 >= x.n_valid) return;
+  const bool whole = r0 + 32 <= x.n_valid;
+  const int es = p.out_f32 ? 4 : 2, per = 64 / es;  // channels in 64 bytes
+  uint8_t* out = static_cast<uint8_t*>(p.out) + (size_t)(x.row0 + r0) * p.N * es;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !p.out_f32) break;
+      const int ch = ch0 + 64 * i + k * per;
+      if (ch >= p.N) break;
+      if (lane == 0) ptx::bulk_wait_read<0>();  // the previous store has read the staged rows
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint4 v;
+        if (p.out_f32) {
+          const float* f = &acc[i][16 * k + 4 * c];
+          v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        } else {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = acc[i][8 * c + j];
+          v = bf16_pack(f);
+        }
+        *reinterpret_cast<uint4*>(outb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v;
+      }
+      if (whole) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_2d(map, ptx::smem_u32(outb), ch, x.row0 + r0);
+          ptx::bulk_commit();
+        }
+        continue;
+      }
+      __syncwarp();
+      const int c = lane & 3;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int r = 8 * h + (lane >> 2);
+        const uint4 t = *reinterpret_cast<const uint4*>(outb + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+        if (r0 + r < x.n_valid && ch + c * (16 / es) < p.N)
+          *reinterpret_cast<uint4*>(out + (size_t)r * p.N * es + (size_t)ch * es + c * 16) = t;
+      }
+      __syncwarp();
+    }
+  }
 }
 
 template <bool TRANS>
@@ -122,31 +306,30 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
   auto accf_bar = [&](int b) { return bars + 8u * (2 * kStages + b); };
   auto acce_bar = [&](int b) { return bars + 8u * (2 * kStages + 2 + b); };
   auto sfull_bar = [&](int i) { return bars + 8u * (2 * kStages + 4 + i); };
-  auto sempty_bar = [&](int i) { return bars + 8u * (2 * kStages + 4 + kScaleSlots + i); };
-  const uint32_t drain_bar = bars + 8u * (2 * kStages + 4 + 2 * kScaleSlots);
+  auto sempty_bar = [&](int i) { return bars + 8u * (2 * kStages + 4 + kScaleRing + i); };
+  const uint32_t drain_bar = bars + 8u * (2 * kStages + 4 + 2 * kScaleRing);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
   int* offs = reinterpret_cast<int*>(smem + kOffsOff);
   int* prefix = reinterpret_cast<int*>(smem + kPrefixOff);
   float* scales = reinterpret_cast<float*>(smem + kScaleOff);
+  float* wscales = reinterpret_cast<float*>(smem + kWScaleOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
-  const bool leader = rank == 0u;
-  auto lead = [&](uint32_t bar) { return ptx::mapa_shared(bar, 0u); };
   const int u_first = (int)(blockIdx.x >> 1), u_step = (int)(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(full_bar(s), 2);  // both producers, on the even CTA's barrier
-      ptx::mbar_init(empty_bar(s), 1);
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 2);  // both CTAs' MMAs: either producer writes into both
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf_bar(b), 1);
-      ptx::mbar_init(acce_bar(b), 2 * kEpiWarps);
+      ptx::mbar_init(acce_bar(b), kEpiWarps);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      ptx::mbar_init(sfull_bar(i), 1);
+    for (int i = 0; i < kScaleRing; ++i) {
+      ptx::mbar_init(sfull_bar(i), 32);  // each lane's copies
       ptx::mbar_init(sempty_bar(i), kEpiWarps);
     }
     ptx::mbar_init(drain_bar, 1);
@@ -158,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
     for (int i = 0; i < 4; ++i) ptx::prefetch_tmap(&maps.a[i]);
   }
   if (warp == 1) {
-    ptx::tmem_alloc<true>(ptx::smem_u32(tmem_slot), 512);
-    ptx::tmem_relinquish<true>();
+    ptx::tmem_alloc<false>(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish<false>();
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -203,137 +386,155 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- copies
       const uint64_t once = ptx::policy_evict_first(), keep = ptx::policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
+      uint32_t used = 0;  // bit j: parity of slot j's uses
       bool ok = true;
-      long long issued = 0;
       for (int u = u_first; u < units && ok; u += u_step) {
         const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
+        // shared rows come in two boxes of 16, 32, 64 or 128 rows, one from each CTA
         const int half = x.n_mma / 2;
         const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
         const CUtensorMap* am = &maps.a[box];
-        const uint32_t bytes = kABytes + (16u << box) * 128u;
-        const int ch = x.mt * 256 + (int)rank * 128, row = x.row0 + (int)rank * half;
+        const uint32_t shared_rows = x.rows_m ? 256u : 32u << box, bytes = kOwnBytes + shared_rows * 128u;
+        const uint32_t w_at = x.rows_m ? kOwnBytes + rank * 16384u : 0u;
+        const uint32_t r_at = x.rows_m ? 0u : kOwnBytes + rank * (2048u << box);
+        const int ch = x.mt * 256 + (int)rank * 128, row = x.row0 + (int)rank * (16 << box);
         const uint64_t pol = x.tiles > 1 ? keep : once;
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, deadline, abort_flag)) {
+          const int stage = kb % kStages;
+          if (!ptx::mbar_wait_bounded(empty_bar(stage), ((used >> stage) & 1u) ^ 1u, deadline, abort_flag)) {
             ok = false;
             break;
           }
-          const uint32_t sa = sbase + stage * kStageBytes, fb = lead(full_bar(stage));
-          ptx::mbar_arrive_expect_tx_cluster(fb, bytes);
-          if (TRANS)
-            ptx::tma_load_box3_pair(sa, &maps.w, fb, ch, kb * 128, x.g, pol);
-          else
-            ptx::tma_load_box3_pair(sa, &maps.w, fb, kb * 128, ch, x.g, pol);
-          ptx::tma_load_2d_pair(sa + kABytes, am, fb, kb * 128, row, keep);
-          ++issued;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+          const uint32_t sa = sbase + stage * kStageBytes, fb = full_bar(stage);
+          const int c0 = TRANS ? ch : kb * 128, c1 = TRANS ? kb * 128 : ch;
+          ptx::mbar_arrive_expect_tx(fb, bytes);
+          if (x.rows_m) {
+            ptx::tma_load_2d(sa, am, fb, kb * 128, row, keep);
+            ptx::tma_load_box3_cast(sa + w_at, &maps.w, fb, c0, c1, x.g, 3, pol);
+          } else {
+            ptx::tma_load_box3(sa, &maps.w, fb, c0, c1, x.g, pol);
+            ptx::tma_load_2d_cast(sa + r_at, am, fb, kb * 128, row, 3, keep);
           }
+          used ^= 1u << stage;
         }
       }
       if (!ok) {
         set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
-        // let issued copies land before shared memory is released
-        const uint64_t now = ptx::globaltimer_ns(), grace = now + 100000000ull;
-        if (leader) {
-          for (long long j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
-            while (!ptx::mbar_try_wait(full_bar((int)(j % kStages)), (uint32_t)((j / kStages) & 1)) &&
-                   ptx::globaltimer_ns() < grace) {
-            }
-        } else {  // this CTA's copies complete the peer's barriers: wait a while
-          while (ptx::globaltimer_ns() < now + 20000000ull) {
+        // let issued copies land before shared memory is released (the peer's
+        // half of a slot may never come: the limit ends the wait)
+        const uint64_t grace = ptx::globaltimer_ns() + 100000000ull;
+        for (int j = 0; j < kStages; ++j)
+          while (!ptx::mbar_try_wait(full_bar(j), ((used >> j) & 1u) ^ 1u) && ptx::globaltimer_ns() < grace) {
           }
-        }
       }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMAs
-      int stage = 0;
-      uint32_t phase = 0, it = 0;
-      bool ok = true;
+      // (the whole warp walks the loop and one elected lane issues: operands
+      // stay in uniform registers, and four MMAs take 100 cycles to issue
+      // instead of 400)
+      const uint32_t one = ptx::elect_one() ? 1u : 0u;
+      uint32_t slots = 0, bufs = 0;  // bit j: parity of the uses of slot j, of buffer j
+      uint32_t next = 0;             // the buffer of a step of four blocks that share one
+      bool ok = true, any = false;
       for (int u = u_first; u < units && ok; u += u_step) {
         const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
-        const uint32_t idesc = ptx::idesc_f16_f32(256, x.n_mma) | (TRANS ? ptx::kIdescAMn : 0u);
-        for (int kb = 0; kb < p.KB; ++kb, ++it) {
-          const uint32_t buf = it & 1u, acc_phase = (it >> 1) & 1u;
-          if (!ptx::mbar_wait_bounded(acce_bar(buf), acc_phase ^ 1u, deadline, abort_flag) ||
-              !ptx::mbar_wait_bounded(full_bar(stage), phase, deadline, abort_flag)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t sa = sbase + stage * kStageBytes;
-          const uint64_t da = TRANS ? ptx::sdesc_mn_sw128(sa, 16384) : ptx::sdesc_k_sw128(sa);
-          const uint64_t db = ptx::sdesc_k_sw128(sa + kABytes);
+        const int n_mma = __shfl_sync(0xffffffffu, x.n_mma, 0), batch = __shfl_sync(0xffffffffu, x.batch, 0);
+        const bool rows_m = batch == 1;
+        const uint32_t idesc =
+            ptx::idesc_f16_f32(128, n_mma) | (!TRANS ? 0u : rows_m ? ptx::kIdescBMn : ptx::kIdescAMn);
+        const uint64_t da0 = TRANS && !rows_m ? ptx::sdesc_mn_sw128(sbase, 16384) : ptx::sdesc_k_sw128(sbase);
+        const uint64_t db0 = TRANS && rows_m ? ptx::sdesc_mn_sw128(sbase + kOwnBytes, 16384)
+                                             : ptx::sdesc_k_sw128(sbase + kOwnBytes);
+        const uint32_t astep = TRANS && !rows_m ? 4096 >> 4 : 2, bstep = TRANS && rows_m ? 4096 >> 4 : 2;
+        // Block j of a step: slot j; buffer j % 2, one for blocks 0, 1 and one
+        // for 2, 3, or one for all four.  A poll takes some 70 cycles, so the
+        // next block's barriers are asked while this block's MMAs run.
+        auto buffer = [&](int j) { return batch == 1 ? (uint32_t)(j & 1) : batch == 2 ? (uint32_t)(j >> 1) : next; };
+        auto polled = [&](int j) {
+          const bool f = ptx::mbar_test_wait(full_bar(j), (slots >> j) & 1u);
+          if (j & (batch - 1)) return f;
+          const uint32_t b = buffer(j);
+          return ptx::mbar_test_wait(acce_bar(b), ((bufs >> b) & 1u) ^ 1u) && f;
+        };
+        const int cols = 256 / batch;
+        bool seen = false;
+        for (int kb0 = 0; kb0 < p.KB && ok; kb0 += kGroup) {
+          const int n = min(kGroup, p.KB - kb0);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 of the block's 128 per instruction
-            ptx::mma_f8_pair(tmem_base + 256u * buf, da + kk * (TRANS ? 4096 >> 4 : 2), db + 2 * kk, idesc, kk > 0);
-          ptx::mma_commit_pair(empty_bar(stage));
-          ptx::mma_commit_pair(accf_bar(buf));
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+          for (int j = 0; j < kGroup; ++j) {
+            if (j >= n || !ok) break;
+            const uint32_t b = buffer(j);
+            if (!seen) {
+              ok = ptx::mbar_wait_bounded(full_bar(j), (slots >> j) & 1u, deadline, abort_flag) &&
+                   ((j & (batch - 1)) != 0 ||
+                    ptx::mbar_wait_bounded(acce_bar(b), ((bufs >> b) & 1u) ^ 1u, deadline, abort_flag));
+            }
+            ok = __all_sync(0xffffffffu, ok) != 0;
+            if (!ok) break;
+            ptx::tc_fence_after();
+            slots ^= 1u << j;
+            const bool last = (j & (batch - 1)) == batch - 1 || j == n - 1;
+            if (last) {
+              bufs ^= 1u << b;
+              next ^= batch == 4 ? 1u : 0u;
+            }
+            const uint32_t d = tmem_base + 256u * b + (uint32_t)((j & (batch - 1)) * cols);
+            const uint64_t da = da0 + (uint32_t)(j * (kStageBytes >> 4)), db = db0 + (uint32_t)(j * (kStageBytes >> 4));
+            ptx::mma_f8_one<false>(one, d, da, db, idesc);  // 32 of the block's 128 per instruction
+            ptx::mma_f8_one<true>(one, d, da + astep, db + bstep, idesc);
+            ptx::mma_f8_one<true>(one, d, da + 2 * astep, db + 2 * bstep, idesc);
+            ptx::mma_f8_one<true>(one, d, da + 3 * astep, db + 3 * bstep, idesc);
+            if (last) ptx::mma_commit_one(one, accf_bar(b));
+            ptx::mma_commit_cast_one(one, empty_bar(j), 3);
+            // (only within the unit: the next one may use the buffers in another way)
+            seen = j + 1 < n ? polled(j + 1) : kb0 + kGroup < p.KB && polled(0);
+            any = true;
           }
         }
       }
-      if (!ok) {
+      if (!ok && one) {
         set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
-        if (it > 0) {  // MMAs in flight end before tensor memory is freed
-          ptx::mma_commit_pair(drain_bar);
+        if (any) {  // MMAs in flight end before tensor memory is freed
+          ptx::mma_commit(drain_bar);
           const uint64_t grace = ptx::globaltimer_ns() + 100000000ull;
           while (!ptx::mbar_try_wait(drain_bar, 0u) && ptx::globaltimer_ns() < grace) {
           }
         }
       }
     } else if (warp == 2) {
-      // ---------------------------------------- sa * sw of each block
+      // ------------------------------------------------- scales, by cp.async
+      // (asynchronous, so that their latency never holds a block back)
       uint32_t it = 0;
       bool ok = true;
-      const bool vec = (p.KB & 3) == 0;
       for (int u = u_first; u < units && ok; u += u_step) {
         const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
-        const int nb = min(x.mt * 2 + (int)rank, p.NB - 1);  // (past N: zero weights, never stored)
-        for (int kb = 0; kb < p.KB && ok; kb += 4) {
-          float v[8][4], w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = min(kb + j, p.KB - 1);
-            w[j] = __ldg(p.w_scales + (TRANS ? ((size_t)x.g * p.KB + k) * p.NB + nb
-                                             : ((size_t)x.g * p.NB + nb) * p.KB + k));
+        // rows on N: all rows, this CTA's 128 channels; rows on M: this CTA's
+        // 128 rows, both halves of the channels.  (Channels past N: zero
+        // weights, never stored.)
+        const int first = x.rows_m ? (int)rank * 128 : 0;
+        const int rows = x.rows_m ? min(128, x.n_valid - first) : x.n_valid;
+        const int nb = min(x.mt * 2 + (x.rows_m ? lane & 1 : (int)rank), p.NB - 1);
+        const float* wp = p.w_scales + (size_t)x.g * p.KB * p.NB + (TRANS ? (size_t)nb : (size_t)nb * p.KB);
+        const float* ap = p.a_scales + (size_t)(x.row0 + first + lane) * p.KB;
+        for (int kb = 0; kb < p.KB; kb += kGroup, ++it) {
+          const uint32_t slot = it % kScaleRing;
+          if (!warp_wait(sempty_bar(slot), ((it / kScaleRing) & 1u) ^ 1u, deadline, abort_flag)) {
+            ok = false;
+            break;
           }
+          const uint32_t to = sbase + kScaleOff + slot * (kGroup * kBN * 4) + lane * 4;
+          const int n = min(kGroup, p.KB - kb);
+          for (int r = lane; r < rows; r += 32)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = lane + 32 * i;
-            const float* src = p.a_scales + (size_t)(x.row0 + r) * p.KB + kb;
-            if (r >= x.n_valid) {
-              v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
-            } else if (vec) {
-              const float4 q = __ldg(reinterpret_cast<const float4*>(src));
-              v[i][0] = q.x; v[i][1] = q.y; v[i][2] = q.z; v[i][3] = q.w;
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[i][j] = kb + j < p.KB ? __ldg(src + j) : 0.f;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kb + j >= p.KB) break;
-            const uint32_t slot = it % kScaleSlots;
-            if (!warp_wait(sempty_bar(slot), ((it / kScaleSlots) & 1u) ^ 1u, deadline, abort_flag)) {
-              ok = false;
-              break;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (32 * i < x.n_mma) scales[slot * kBN + lane + 32 * i] = v[i][j] * w[j];
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sfull_bar(slot));
-            ++it;
-          }
+            for (int j = 0; j < kGroup; ++j)
+              if (j < n) ptx::cp_async4(to + (uint32_t)(j * kBN + r - lane) * 4, ap + (size_t)(r - lane) * p.KB + kb + j);
+          if ((lane >> 1) < n)  // lane: block lane / 2, channel half lane & 1
+            ptx::cp_async4(sbase + kWScaleOff + slot * (kGroup * 8) + lane * 4,
+                           wp + (size_t)(kb + (lane >> 1)) * (TRANS ? p.NB : 1));
+          ptx::cp_async_arrive_noinc(sfull_bar(slot));
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok && lane == 0) set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
     }
   } else {
@@ -341,110 +542,83 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
     ptx::regs_inc<kRegsHigh>();
     const int q = warp & 3, eg = (warp - 4) >> 2;
     uint8_t* outb = smem + kOutOff + (warp - 4) * kOutBytes;
-    const uint32_t out_s = ptx::smem_u32(outb);
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
-    uint32_t it = 0;
+    const Accumulate step{tlane + eg * 32, eg * 32, q * 32 + lane};
+    uint32_t sit = 0, bufs = 0, next = 0;  // (bufs, next: as the MMA warp has them)
     bool ok = true;
     for (int u = u_first; u < units; u += u_step) {
-      const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
-      // acc[chunk][lane half][column group][lane + 0 / 8]: pairs of rows
-      uint64_t acc[4][2][4][2];
+      int n_mma, batch;
+      {
+        const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
+        n_mma = x.n_mma;
+        batch = x.batch;
+      }
+      float acc[kChunks][32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][h][j][0] = acc[i][h][j][1] = 0ull;
-      for (int kb = 0; kb < p.KB; ++kb, ++it) {
-        const uint32_t buf = it & 1u, slot = it % kScaleSlots;
-        if (!warp_wait(sfull_bar(slot), (it / kScaleSlots) & 1u, deadline, abort_flag) ||
-            !warp_wait(accf_bar(buf), (it >> 1) & 1u, deadline, abort_flag)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const float* sc = scales + slot * kBN + 2 * (lane & 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c0 = (2 * i + eg) * 32;
-          if (c0 < x.n_mma) {
-            uint32_t d0[16], d1[16];
-            ptx::tmem_ld_16x256b_x4(tlane + 256u * buf + c0, d0);
-            ptx::tmem_ld_16x256b_x4(tlane + (16u << 16) + 256u * buf + c0, d1);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 s = *reinterpret_cast<const float2*>(sc + c0 + 8 * j);
-              const uint64_t s2 = ptx::pack_f32x2(__float_as_uint(s.x), __float_as_uint(s.y));
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                acc[i][0][j][r] =
-                    ptx::fma_f32x2(ptx::pack_f32x2(d0[4 * j + 2 * r], d0[4 * j + 2 * r + 1]), s2, acc[i][0][j][r]);
-                acc[i][1][j][r] =
-                    ptx::fma_f32x2(ptx::pack_f32x2(d1[4 * j + 2 * r], d1[4 * j + 2 * r + 1]), s2, acc[i][1][j][r]);
-              }
-            }
+        for (int j = 0; j < 32; ++j) acc[i][j] = 0.f;
+      for (int kb0 = 0; kb0 < p.KB && ok; kb0 += kGroup, ++sit) {
+        const uint32_t group = sit % kScaleRing;
+        ok = warp_wait(sfull_bar(group), (sit / kScaleRing) & 1u, deadline, abort_flag);
+        if (!ok) break;
+        const float* sc = scales + group * kGroup * kBN;
+        const float* ws = wscales + group * kGroup * 2;
+        const int n = min(kGroup, p.KB - kb0);
+        auto arrived = [&](uint32_t b) { return ptx::mbar_test_wait(accf_bar(b), (bufs >> b) & 1u); };
+        auto acquire = [&](uint32_t b, bool seen) {  // buffer b is full
+          seen = __all_sync(0xffffffffu, seen) || warp_wait(accf_bar(b), (bufs >> b) & 1u, deadline, abort_flag);
+          ptx::tc_fence_after();
+          return seen;
+        };
+        auto release = [&](uint32_t b) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(acce_bar(b));
+          bufs ^= 1u << b;
+        };
+        if (batch == 1) {
+          bool seen = arrived(0);
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            const float f = sc[j * kBN + step.row], f0 = f * ws[2 * j], f1 = f * ws[2 * j + 1];
+            const uint32_t b = j & 1;
+            ok = acquire(b, seen);
+            if (!ok) break;
+            step.rows_m(acc, b, f0, f1, [&] {
+              release(b);
+              seen = arrived(b ^ 1u);  // (the answer comes while the last columns are added)
+            });
+          }
+        } else if (batch == 2) {
+          for (int j = 0; j < n; j += 2) {
+            const uint32_t b = j >> 1;
+            ok = acquire(b, arrived(b));
+            if (!ok) break;
+            step.rows_n<2>(acc, b, min(2, n - j), n_mma, sc + j * kBN, ws + 2 * j);
+            release(b);
+          }
+        } else {
+          ok = acquire(next, arrived(next));
+          if (ok) {
+            step.rows_n<4>(acc, next, n, n_mma, sc, ws);
+            release(next);
+            next ^= 1u;
           }
         }
-        ptx::tc_fence_before();
+        if (!ok) break;
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive_cluster(lead(acce_bar(buf)));
-          ptx::mbar_arrive(sempty_bar(slot));
-        }
+        if (lane == 0) ptx::mbar_arrive(sempty_bar(group));
       }
       if (!ok) break;
-      const int ch0 = x.mt * 256 + (int)rank * 128 + q * 32;
-      if (ch0 >= p.N) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c0 = (2 * i + eg) * 32;
-        if (c0 >= x.n_valid) break;
-        if (p.out_f32) {
-          float* out = static_cast<float*>(p.out);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                float lo, hi;
-                ptx::unpack_f32x2(acc[i][h][j][r], lo, hi);
-                const int ch = ch0 + 16 * h + 8 * r + (lane >> 2), c = c0 + 8 * j + 2 * (lane & 3);
-                if (ch < p.N) {
-                  float* to = out + (size_t)(x.row0 + c) * p.N + ch;
-                  if (c < x.n_valid) to[0] = lo;
-                  if (c + 1 < x.n_valid) to[p.N] = hi;
-                }
-              }
-        } else {
-          // rows of 32 channels through shared memory: 16-byte stores
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t m[4];
-#pragma unroll
-            for (int o = 0; o < 4; ++o) {  // channels 8o .. 8o + 7
-              float lo, hi;
-              ptx::unpack_f32x2(acc[i][o >> 1][j][o & 1], lo, hi);
-              const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-              m[o] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            ptx::stmatrix_x4_trans(out_s + (8 * j + (lane & 7)) * kOutPitch + (lane >> 3) * 16, m[0], m[1], m[2], m[3]);
-          }
-          __syncwarp();
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-          const int ch = ch0 + (lane & 3) * 8;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = 8 * k + (lane >> 2), c = c0 + rr;
-            const uint4 v = *reinterpret_cast<const uint4*>(outb + rr * kOutPitch + (lane & 3) * 16);
-            if (c < x.n_valid && ch < p.N)
-              *reinterpret_cast<uint4*>(out + (size_t)(x.row0 + c) * p.N + ch) = v;
-          }
-          __syncwarp();
-        }
-      }
+      // (worked out again: the registers hold sums during the loop)
+      const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
+      if (x.rows_m)
+        store_rows_m(p, &maps.out, x, acc, (int)rank * 128 + q * 32, x.mt * 256 + eg * 32, outb);
+      else
+        store_rows_n(p, x, acc, x.mt * 256 + (int)rank * 128 + q * 32, eg * 32, outb);
     }
+    if (lane == 0) ptx::bulk_wait_all();
     if (!ok && lane == 0) set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
   }
 
@@ -453,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc<true>(tmem_base, 512);
+    ptx::tmem_dealloc<false>(tmem_base, 512);
   }
 }
 
@@ -526,6 +700,8 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
   else
     MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.N, a.K, a.K, 1, 128, 128, 128));
   for (int i = 0; i < 4; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K, 1, 16u << i, 128, 128));
+  const int es = a.out_f32 ? 4 : 2;
+  MOE_TRY(make_tmap_2d(&maps.out, a.out, a.R, a.N, es, 32, 64 / es, 64));
   return a.transposed ? launch<true>(p, maps, a.num_sms, s) : launch<false>(p, maps, a.num_sms, s);
 }
 

@@ -60,7 +60,7 @@ inline moe_status cuda_status(cudaError_t err) {
   } while (0)
 
 // 2-D row-major tensor map for TMA: `rows` x `cols` elements of
-// `elem_bytes` (2: bf16, 1: bytes), row pitch `cols * elem_bytes`, box
+// `elem_bytes` (4: fp32, 2: bf16, 1: bytes), row pitch `cols * elem_bytes`, box
 // `box_cols` x `box_rows`, swizzle of `swizzle_bytes` (128, 64 or 0: none),
 // zero fill out of bounds.
 moe_status make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,

@@ -115,8 +115,9 @@ moe_status make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint6
   }
   if ((reinterpret_cast<uintptr_t>(base) & 15u) != 0 || ((cols * elem_bytes) & 15u) != 0)
     return MOE_ERR_INVALID_ARG;
-  CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                           : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMapDataType dt = elem_bytes == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                           : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * (cuuint64_t)elem_bytes};
   cuuint32_t box[2] = {box_cols, box_rows};

@@ -346,22 +346,27 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
           break;
         }
         ptx::tc_fence_after();
+        const uint32_t at = tlane + 256u * buf + eg * 32;
+        uint32_t d[2][16];
+        ptx::tmem_ld16(at, d[0]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t d0[16], d1[16];
-          const uint32_t at = tlane + 256u * buf + (2 * i + eg) * 32;
-          ptx::tmem_ld16(at, d0);
-          ptx::tmem_ld16(at + 16, d1);
-          ptx::tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            acc[i][j] = ptx::add_f32x2(acc[i][j], ptx::pack_f32x2(d0[2 * j], d0[2 * j + 1]));
-            acc[i][8 + j] = ptx::add_f32x2(acc[i][8 + j], ptx::pack_f32x2(d1[2 * j], d1[2 * j + 1]));
+          for (int h = 0; h < 2; ++h) {  // the next 16 columns are on their way while 16 are added
+            const int n = 2 * i + h, next = n + 1;
+            ptx::tmem_ld_wait(d[h]);
+            if (next < 8) {
+              ptx::tmem_ld16(at + (next >> 1) * 64 + (next & 1) * 16, d[h ^ 1]);
+            } else {  // everything is in registers: the buffer can fill again
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive_cluster(lead(acce_bar(buf)));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[i][8 * h + j] = ptx::add_f32x2(acc[i][8 * h + j], ptx::pack_f32x2(d[h][2 * j], d[h][2 * j + 1]));
           }
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(lead(acce_bar(buf)));
       }
       if (!ok) break;
       const int n0 = x.nt * 256 + (int)rank * 128 + q * 32;
