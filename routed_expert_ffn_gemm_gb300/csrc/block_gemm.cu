@@ -139,20 +139,19 @@ struct Accumulate {
   template <typename Release>
   __device__ __forceinline__ void rows_m(float (&acc)[kChunks][32], uint32_t buf, float f0, float f1,
                                          Release release) const {
-    uint32_t d[2][16];
+    uint32_t d[2][32];
     const uint32_t from = at + 256u * buf;
-    ptx::tmem_ld16(from, d[0]);
+    ptx::tmem_ld32(from, d[0]);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      ptx::tmem_ld_wait(d[t & 1]);
-      if (t < 7)
-        ptx::tmem_ld16(from + 64u * ((t + 1) >> 1) + 16u * ((t + 1) & 1), d[(t + 1) & 1]);
+    for (int t = 0; t < 4; ++t) {
+      ptx::tmem_ld_wait();
+      if (t < 3)
+        ptx::tmem_ld32(from + 64u * (t + 1), d[(t + 1) & 1]);
       else
         release();
-      const float f = t < 4 ? f0 : f1;
-      float* a = acc[t >> 1] + 16 * (t & 1);
+      const float f = t < 2 ? f0 : f1;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) a[j] = fmaf(__uint_as_float(d[t & 1][j]), f, a[j]);
+      for (int j = 0; j < 32; ++j) acc[t][j] = fmaf(__uint_as_float(d[t & 1][j]), f, acc[t][j]);
     }
   }
 
@@ -168,7 +167,7 @@ struct Accumulate {
       if (live(t)) {
         uint32_t d[32];
         ptx::tmem_ld32(at + 256u * buf + 64u * t, d);
-        ptx::tmem_ld_wait(d);
+        ptx::tmem_ld_wait();
         const float w = ws[2 * (t / PER)];
         const float* s = sc + (t / PER) * kBN + (t % PER) * 64 + first;
 #pragma unroll

@@ -39,23 +39,27 @@ constexpr int kChunkStages = 4;               // stages summed in tensor memory
 constexpr int kTileBytes = kRows * 128 * 2;   // 128 columns of 64 rows, bf16: two 64-column halves
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kCodeBytes = kRows * 128;
-constexpr int kStages = 4;
-constexpr int kStageBytes = 2 * kTileBytes + kCodeBytes;
 constexpr int kEpiWarps = 8, kPrepWarps = 4;
 constexpr int kBand = 8;
 constexpr int kMaxGroups = 1024;
-constexpr int kOutBytes = 32 * 128;           // per accumulating warp: 32 x 32 fp32
-constexpr int kOutOff = kStages * kStageBytes;
-constexpr int kBarOff = kOutOff + kEpiWarps * kOutBytes;
-// full[S], ready[S], empty[S], acc_full[2], acc_empty[2], drain
-constexpr int kNumBars = 3 * kStages + 5;
-constexpr int kSlotOff = kBarOff + 8 * kNumBars + 8;
-constexpr int kAbortOff = kSlotOff + 8;
-constexpr int kOffsOff = kAbortOff + 8;
-constexpr int kSmemBytes = kOffsOff + 4 * (kMaxGroups + 4) + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
-// every CTA holds all of its SM's tensor memory: never two on one SM
-static_assert(2 * (kSmemBytes + 1024) > 232448 + 1024, "one CTA per SM");
+constexpr int kOutBytes = 32 * 64;            // per accumulating warp: 32 rows of 64 bytes
+
+template <bool CODES>
+struct Smem {
+  static constexpr int STAGES = CODES ? 5 : 6;
+  static constexpr int STAGE_BYTES = 2 * kTileBytes + (CODES ? kCodeBytes : 0);
+  static constexpr int OUT_OFF = STAGES * STAGE_BYTES;
+  static constexpr int BAR_OFF = OUT_OFF + kEpiWarps * kOutBytes;
+  // full[S], ready[S], empty[S], acc_full[2], acc_empty[2], drain
+  static constexpr int NUM_BARS = 3 * STAGES + 5;
+  static constexpr int SLOT_OFF = BAR_OFF + 8 * NUM_BARS + 8;
+  static constexpr int ABORT_OFF = SLOT_OFF + 8;
+  static constexpr int OFFS_OFF = ABORT_OFF + 8;
+  static constexpr int BYTES = OFFS_OFF + 4 * (kMaxGroups + 4) + 1024;
+  static_assert(BYTES <= 232448, "shared memory budget");
+  // every CTA holds all of its SM's tensor memory: never two on one SM
+  static_assert(2 * (BYTES + 1024) > 232448 + 1024, "one CTA per SM");
+};
 constexpr int kRegsLow = 40, kRegsPrep = 80, kRegsHigh = 192;
 static_assert(128 * (kRegsLow + kRegsPrep + 2 * kRegsHigh) <= kThreads * 128, "register split");
 
@@ -97,20 +101,22 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 
 template <bool CODES>
 __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, const __grid_constant__ Maps maps) {
+  using S = Smem<CODES>;
+  constexpr int kStages = S::STAGES, kStageBytes = S::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = ptx::smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
-  const uint32_t sbase = raw_s + pad, bars = sbase + kBarOff;
+  const uint32_t sbase = raw_s + pad, bars = sbase + S::BAR_OFF;
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto ready_bar = [&](int s) { return bars + 8u * (kStages + s); };
   auto empty_bar = [&](int s) { return bars + 8u * (2 * kStages + s); };
   auto accf_bar = [&](int b) { return bars + 8u * (3 * kStages + b); };
   auto acce_bar = [&](int b) { return bars + 8u * (3 * kStages + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (3 * kStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
-  int* offs = reinterpret_cast<int*>(smem + kOffsOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::SLOT_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::ABORT_OFF);
+  int* offs = reinterpret_cast<int*>(smem + S::OFFS_OFF);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
@@ -204,43 +210,45 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
                  ptx::globaltimer_ns() < grace) {
           }
       }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
       // ------------------------------------------------------------ MMAs
+      // (the whole warp walks the loop and one elected lane issues)
+      const uint32_t one = ptx::elect_one() ? 1u : 0u;
       const uint32_t idesc = ptx::idesc_bf16_f32(256, 256) | ptx::kIdescAMn | ptx::kIdescBMn;
+      const uint64_t da0 = ptx::sdesc_mn_sw128(sbase, kHalfBytes);
+      const uint64_t db0 = ptx::sdesc_mn_sw128(sbase + kTileBytes, kHalfBytes);
       int stage = 0;
       uint32_t phase = 0, it = 0;
-      bool ok = true, any = false;
+      bool ok = true, any = false, seen = false;
       for (int u = u_first; u < units && ok; u += u_step) {
         const Unit x = unit_of(u, offs, p);
         for (int s = 0; s < x.stages; ++s) {
           const uint32_t buf = it & 1u;
           const bool first = s % kChunkStages == 0;
-          if ((first && !ptx::mbar_wait_bounded(acce_bar(buf), ((it >> 1) & 1u) ^ 1u, deadline, abort_flag)) ||
-              !ptx::mbar_wait_bounded(ready_bar(stage), phase, deadline, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = (!first || ptx::mbar_wait_bounded(acce_bar(buf), ((it >> 1) & 1u) ^ 1u, deadline, abort_flag)) &&
+               (seen || ptx::mbar_wait_bounded(ready_bar(stage), phase, deadline, abort_flag));
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t sa = sbase + stage * kStageBytes;
-          const uint64_t da = ptx::sdesc_mn_sw128(sa, kHalfBytes);
-          const uint64_t db = ptx::sdesc_mn_sw128(sa + kTileBytes, kHalfBytes);
+          const uint64_t da = da0 + (uint32_t)(stage * (kStageBytes >> 4)), db = db0 + (uint32_t)(stage * (kStageBytes >> 4));
+          const uint32_t d = tmem_base + 256u * buf;
           const int steps = (min(kRows, x.rows - s * kRows) + 15) / 16;
           for (int kk = 0; kk < steps; ++kk)  // 16 rows (two 8-row groups) per instruction
-            ptx::mma_f16_pair(tmem_base + 256u * buf, da + kk * (2048 >> 4), db + kk * (2048 >> 4), idesc,
-                              !first || kk > 0);
+            ptx::mma_f16_pair_one(one, d, da + kk * (2048 >> 4), db + kk * (2048 >> 4), idesc, !first || kk > 0);
           any = true;
-          ptx::mma_commit_pair(empty_bar(stage));
+          ptx::mma_commit_pair_one(one, empty_bar(stage));
           if (s % kChunkStages == kChunkStages - 1 || s == x.stages - 1) {
-            ptx::mma_commit_pair(accf_bar(buf));
+            ptx::mma_commit_pair_one(one, accf_bar(buf));
             ++it;
           }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
+          seen = ptx::mbar_test_wait(ready_bar(stage), phase);  // (the answer comes while the MMAs run)
         }
       }
-      if (!ok) {
+      if (!ok && one) {
         set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
         if (any) {
           ptx::mma_commit_pair(drain_bar);
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
     // ------------------------------------------------------- accumulation
     ptx::regs_inc<kRegsHigh>();
     const int q = warp & 3, eg = (warp - 8) >> 2;
-    uint8_t* outb = smem + kOutOff + (warp - 8) * kOutBytes;
+    uint8_t* outb = smem + S::OUT_OFF + (warp - 8) * kOutBytes;
     const uint32_t out_s = ptx::smem_u32(outb);
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
     uint32_t it = 0;
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // the next 16 columns are on their way while 16 are added
             const int n = 2 * i + h, next = n + 1;
-            ptx::tmem_ld_wait(d[h]);
+            ptx::tmem_ld_wait();
             if (next < 8) {
               ptx::tmem_ld16(at + (next >> 1) * 64 + (next & 1) * 16, d[h ^ 1]);
             } else {  // everything is in registers: the buffer can fill again
@@ -371,37 +379,42 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
       if (!ok) break;
       const int n0 = x.nt * 256 + (int)rank * 128 + q * 32;
       if (n0 >= p.N) continue;
+      const int per = p.out_f32 ? 16 : 32;  // columns in 64 bytes
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int k0 = x.kt * 256 + (2 * i + eg) * 32;
-        if (k0 >= p.K) break;
-        if (lane == 0) ptx::bulk_wait_read<0>();  // the previous box has left the buffer
-        __syncwarp();
-        if (p.out_f32) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float4 v;
-            ptx::unpack_f32x2(acc[i][2 * c], v.x, v.y);
-            ptx::unpack_f32x2(acc[i][2 * c + 1], v.z, v.w);
-            *reinterpret_cast<float4*>(outb + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
-          }
-        } else {
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !p.out_f32) break;
+          const int k0 = x.kt * 256 + (2 * i + eg) * 32 + h * per;
+          if (k0 >= p.K) break;
+          if (lane == 0) ptx::bulk_wait_read<0>();  // the previous box has left the buffer
+          __syncwarp();
+          // 16-byte chunk c of row r at c ^ ((r >> 1) & 3): the box' 64-byte swizzle
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float v[8];
+            uint4 v;
+            if (p.out_f32) {
+              float4 f;
+              ptx::unpack_f32x2(acc[i][8 * h + 2 * c], f.x, f.y);
+              ptx::unpack_f32x2(acc[i][8 * h + 2 * c + 1], f.z, f.w);
+              v = *reinterpret_cast<const uint4*>(&f);
+            } else {
+              float f[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ptx::unpack_f32x2(acc[i][4 * c + j], v[2 * j], v[2 * j + 1]);
-            *reinterpret_cast<uint4*>(outb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = bf16_pack(v);
+              for (int j = 0; j < 4; ++j) ptx::unpack_f32x2(acc[i][4 * c + j], f[2 * j], f[2 * j + 1]);
+              v = bf16_pack(f);
+            }
+            *reinterpret_cast<uint4*>(outb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v;
           }
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (p.accumulate)
-            ptx::tma_add_box3(&maps.dw, out_s, k0, n0, x.g);
-          else
-            ptx::tma_store_box3(&maps.dw, out_s, k0, n0, x.g);
-          ptx::bulk_commit();
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (p.accumulate)
+              ptx::tma_add_box3(&maps.dw, out_s, k0, n0, x.g);
+            else
+              ptx::tma_store_box3(&maps.dw, out_s, k0, n0, x.g);
+            ptx::bulk_commit();
+          }
         }
       }
     }
@@ -429,11 +442,11 @@ moe_status launch(const Params& p, const Maps& maps, int num_sms, cudaStream_t s
   if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
   int n = known[dev].load(std::memory_order_relaxed);
   if (n == 0) {
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<CODES>::BYTES));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = Smem<CODES>::BYTES;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -448,7 +461,7 @@ moe_status launch(const Params& p, const Maps& maps, int num_sms, cudaStream_t s
   const long long units = (long long)p.E * p.NT * p.KT;
   int grid = 2 * n < num_sms ? 2 * n : num_sms & ~1;
   if (2 * units < grid) grid = (int)(2 * units);
-  MOE_TRY_CUDA(launch_kc(2, kern, dim3(grid), dim3(kThreads), kSmemBytes, s, p, maps));
+  MOE_TRY_CUDA(launch_kc(2, kern, dim3(grid), dim3(kThreads), Smem<CODES>::BYTES, s, p, maps));
   return MOE_OK;
 }
 
@@ -478,7 +491,7 @@ moe_status grouped_wgrad_launch(const WgradArgs& a, cudaStream_t s) {
   else
     MOE_TRY(make_tmap_3d(&maps.x, a.x, 1, a.R, a.K, (uint64_t)a.K * 2, 2, kRows, 64, 128));
   const int es = a.out_f32 ? 4 : 2;
-  MOE_TRY(make_tmap_3d(&maps.dw, a.dw, a.E, a.N, a.K, (uint64_t)a.K * es, es, 32, 32, 32 * es));
+  MOE_TRY(make_tmap_3d(&maps.dw, a.dw, a.E, a.N, a.K, (uint64_t)a.K * es, es, 32, 64 / es, 64));
   return codes ? launch<true>(p, maps, a.num_sms, s) : launch<false>(p, maps, a.num_sms, s);
 }
 
