@@ -15,13 +15,16 @@
 // atomics, so every run gives the same bits.
 #include <math.h>
 
+#include "ptx.cuh"
 #include "train.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;       // gradient
 constexpr int kWarps = kThreads / 32;
+constexpr int kSumThreads = 1024;   // sum over the CTAs' parts: clusters of
+constexpr int kSumCtas = 8;         // this many CTAs share the experts
 
 // Lanes LG hold a row: lane l has columns (i * LG + l) * VEC + c.
 template <int LG, int VEC, int NI>
@@ -61,80 +64,64 @@ __device__ __forceinline__ float group_max(float v) {
 // lse^2 (float), unmasked tokens (int).
 __host__ __device__ inline size_t part_words(int E) { return 2 * (size_t)E + 2; }
 
-// Sums the CTAs' parts in CTA order and writes counts and losses.  One CTA.
-__device__ void finalize(const RouterLossArgs& a, const uint32_t* parts, int nparts) {
-  __shared__ float red_p[kThreads], red_z[kWarps];
-  __shared__ int red_n[kWarps];
-  const size_t pw = part_words(a.E);
-  float zs = 0.f;
-  int n = 0;
-  for (int b = threadIdx.x; b < nparts; b += kThreads) {
-    zs += __uint_as_float(__ldcg(parts + b * pw + 2 * a.E));
-    n += (int)__ldcg(parts + b * pw + 2 * a.E + 1);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    zs += __shfl_xor_sync(0xffffffffu, zs, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    red_z[threadIdx.x >> 5] = zs;
-    red_n[threadIdx.x >> 5] = n;
-  }
-  __syncthreads();
-  zs = 0.f;
-  n = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    zs += red_z[w];
-    n += red_n[w];
-  }
-  float dot = 0.f;  // sum over this thread's experts of counts_e * P_e
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    float P = 0.f;
-    int c = 0;
-    for (int b = 0; b < nparts; ++b) {
-      P += __uint_as_float(__ldcg(parts + b * pw + e));
-      c += (int)__ldcg(parts + b * pw + a.E + e);
-    }
-    a.counts[e] = c;
-    dot += (float)c * P;
-  }
-  red_p[threadIdx.x] = dot;
-  __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) red_p[threadIdx.x] += red_p[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    const float fn = (float)n;
-    a.counts[a.E] = n;
-    a.loss[0] = n > 0 ? a.balance * (float)a.E * (red_p[0] / (fn * (float)a.k)) / fn : 0.f;
-    a.loss[1] = n > 0 ? a.z * (zs / fn) : 0.f;
-  }
+// Losses from the sums over tokens.
+__device__ __forceinline__ void write_losses(const RouterLossArgs& a, float dot, float zs, int n) {
+  const float fn = (float)n;
+  a.counts[a.E] = n;
+  a.loss[0] = n > 0 ? a.balance * (float)a.E * (dot / (fn * (float)a.k)) / fn : 0.f;
+  a.loss[1] = n > 0 ? a.z * (zs / fn) : 0.f;
 }
 
-template <int LG, int VEC, int NI>
-__global__ void __launch_bounds__(kThreads) router_losses_kernel(const RouterLossArgs a) {
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Sum over the block in a fixed order, known to every thread.
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T* red) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  T s = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += red[w];
+  return s;
+}
+
+// THREADS: many warps on each SM (rows wait for memory), as registers allow.
+template <int LG, int VEC, int NI, int THREADS>
+__global__ void __launch_bounds__(THREADS) router_losses_kernel(const RouterLossArgs a) {
   griddep_begin();
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ uint32_t sm[];
-  float* psum = reinterpret_cast<float*>(sm);                 // [kWarps][E]
-  int* hist = reinterpret_cast<int*>(sm + kWarps * a.E);      // [E]
-  __shared__ float red_z[kWarps];
-  __shared__ int red_n[kWarps];
+  float* psum = reinterpret_cast<float*>(sm);                 // [WARPS][E]
+  int* hist = reinterpret_cast<int*>(sm + WARPS * a.E);       // [E]
+  __shared__ float red_f[WARPS];
+  __shared__ int red_n[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (LG - 1);
   constexpr int RPW = 32 / LG;  // rows of a warp at a time
-  for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += THREADS) hist[e] = 0;
   __syncthreads();
   float P[NI * VEC], zs = 0.f;
   int n = 0;
 #pragma unroll
   for (int i = 0; i < NI * VEC; ++i) P[i] = 0.f;
-  const int step = gridDim.x * kWarps * RPW;
-  for (int t0 = (blockIdx.x * kWarps + warp) * RPW; t0 < a.T; t0 += step) {
+  const int step = gridDim.x * WARPS * RPW;
+  for (int t0 = (blockIdx.x * WARPS + warp) * RPW; t0 < a.T; t0 += step) {
     const int t = t0 + lane / LG;
     const bool here = t < a.T, live = here && (a.mask == nullptr || a.mask[t] != 0);
     Row<LG, VEC, NI> r;
     if (here) r.load(a.logits + (size_t)t * a.E, a.E, l);
+    if (live)
+      for (int j = l; j < a.k; j += LG) {
+        const int e = a.idx[(size_t)t * a.k + j];
+        if (e >= 0 && e < a.E)
+          atomicAdd(hist + e, 1);
+        else
+          set_device_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NI * VEC; ++i) {
@@ -160,19 +147,6 @@ __global__ void __launch_bounds__(kThreads) router_losses_kernel(const RouterLos
       if (l == 0) zs = fmaf(lse, lse, zs);
     }
     if (live && l == 0) ++n;
-    if (live)
-      for (int j = l; j < a.k; j += LG) {
-        const int e = a.idx[(size_t)t * a.k + j];
-        if (e >= 0 && e < a.E)
-          atomicAdd(hist + e, 1);
-        else
-          set_device_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-      }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    zs += __shfl_xor_sync(0xffffffffu, zs, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
   }
 #pragma unroll
   for (int i = 0; i < NI * VEC; ++i) {
@@ -181,37 +155,79 @@ __global__ void __launch_bounds__(kThreads) router_losses_kernel(const RouterLos
     const int e = Row<LG, VEC, NI>::col(i / VEC, l) + i % VEC;
     if (lane < LG && e < a.E) psum[warp * a.E + e] = P[i];
   }
-  if (lane == 0) {
-    red_z[warp] = zs;
-    red_n[warp] = n;
-  }
-  __syncthreads();
+  zs = block_sum(zs, red_f);  // (its barriers: the sums and counts of all warps are written)
+  n = block_sum(n, red_n);
   uint32_t* part = static_cast<uint32_t*>(a.workspace) + blockIdx.x * part_words(a.E);
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+  const bool alone = gridDim.x == 1;
+  float dot = 0.f;
+  for (int e = threadIdx.x; e < a.E; e += THREADS) {
     float s = 0.f;
-    for (int w = 0; w < kWarps; ++w) s += psum[w * a.E + e];
-    part[e] = __float_as_uint(s);
-    part[a.E + e] = (uint32_t)hist[e];
-  }
-  if (threadIdx.x == 0) {
-    float s = 0.f;
-    int c = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      s += red_z[w];
-      c += red_n[w];
+    for (int w = 0; w < WARPS; ++w) s += psum[w * a.E + e];
+    if (alone) {
+      a.counts[e] = hist[e];
+      dot += (float)hist[e] * s;
+    } else {
+      part[e] = __float_as_uint(s);
+      part[a.E + e] = (uint32_t)hist[e];
     }
-    part[2 * a.E] = __float_as_uint(s);
-    part[2 * a.E + 1] = (uint32_t)c;
   }
-  if (gridDim.x == 1) {
-    __syncthreads();
-    finalize(a, part, 1);
+  if (alone) {
+    dot = block_sum(dot, red_f);
+    if (threadIdx.x == 0) write_losses(a, dot, zs, n);
+  } else if (threadIdx.x == 0) {
+    part[2 * a.E] = __float_as_uint(zs);
+    part[2 * a.E + 1] = (uint32_t)n;
   }
 }
 
-__global__ void __launch_bounds__(kThreads) router_losses_finalize_kernel(const RouterLossArgs a, int nparts) {
+// Sums the parts in a fixed order: one cluster, its CTAs taking E / 8 experts
+// each, 32 threads an expert; the first CTA adds their shares of
+// sum_e c_e P_e through distributed shared memory.
+__global__ void __launch_bounds__(kSumThreads) __cluster_dims__(kSumCtas, 1, 1)
+    router_losses_sum_kernel(const RouterLossArgs a, int nparts) {
   griddep_begin();
-  finalize(a, static_cast<const uint32_t*>(a.workspace), nparts);
+  __shared__ float red[kSumThreads / 32];
+  __shared__ int red_n[kSumThreads / 32];
+  __shared__ float shares[kSumCtas];
+  const uint32_t* parts = static_cast<const uint32_t*>(a.workspace);
+  const size_t pw = part_words(a.E);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x;
+  float dot = 0.f;
+  for (int e = rank * (kSumThreads / 32) + warp; e < a.E; e += kSumCtas * (kSumThreads / 32)) {
+    float P = 0.f;
+    int c = 0;
+    for (int b = lane; b < nparts; b += 32) {
+      P += __uint_as_float(__ldcg(parts + b * pw + e));
+      c += (int)__ldcg(parts + b * pw + a.E + e);
+    }
+    P = warp_sum(P);
+    c = warp_sum(c);
+    if (lane == 0) {
+      a.counts[e] = c;
+      dot += (float)c * P;
+    }
+  }
+  dot = block_sum(dot, red);
+  float zs = 0.f;
+  int n = 0;
+  if (rank == 0) {
+    for (int b = threadIdx.x; b < nparts; b += kSumThreads) {
+      zs += __uint_as_float(__ldcg(parts + b * pw + 2 * a.E));
+      n += (int)__ldcg(parts + b * pw + 2 * a.E + 1);
+    }
+    zs = block_sum(zs, red);
+    n = block_sum(n, red_n);
+  }
+  if (threadIdx.x == 0) {
+    const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&shares[rank]), 0u);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(dot) : "memory");
+  }
+  ptx::cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    float s = 0.f;
+    for (int r = 0; r < kSumCtas; ++r) s += shares[r];
+    write_losses(a, s, zs, n);
+  }
 }
 
 template <int LG, int VEC, int NI>
@@ -312,17 +328,21 @@ moe_status dispatch(int E, const Args& a, int blocks, cudaStream_t s) {
   if (E <= 512) return Launch<32, 1, 16>::run(a, blocks, s);
   return Launch<32, 1, 32>::run(a, blocks, s);
 }
-// Rows a CTA holds at a time under dispatch()'s layouts.
-int rows_per_pass(int E) {
-  const int lg = E <= 32 ? 8 : E % 4 == 0 && E <= 64 ? 16 : 32;
-  return kThreads / lg;
-}
+// Lanes that hold a row under dispatch()'s layouts.
+int lanes_of_row(int E) { return E <= 32 ? 8 : E % 4 == 0 && E <= 64 ? 16 : 32; }
+// Threads of the forward's CTAs: 64 registers a thread hold rows of up to 512
+// logits beside their sums.
+constexpr int forward_threads(int per_lane) { return per_lane <= 16 ? 1024 : 512; }
+int forward_threads_of(int E) { return E > 512 ? 512 : 1024; }
 
 template <int LG, int VEC, int NI>
 struct Forward {
   static moe_status run(const RouterLossArgs& a, int blocks, cudaStream_t s) {
-    const size_t smem = 4 * (size_t)(kWarps + 1) * a.E;
-    MOE_TRY_CUDA(launch_k(router_losses_kernel<LG, VEC, NI>, dim3(blocks), dim3(kThreads), smem, s, a));
+    constexpr int THREADS = forward_threads(NI * VEC);
+    const size_t smem = 4 * (size_t)(THREADS / 32 + 1) * a.E;
+    auto kern = router_losses_kernel<LG, VEC, NI, THREADS>;
+    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    MOE_TRY_CUDA(launch_k(kern, dim3(blocks), dim3(THREADS), smem, s, a));
     return MOE_OK;
   }
 };
@@ -336,7 +356,7 @@ struct Backward {
 };
 
 int forward_blocks(int T, int E, int num_sms) {
-  const int want = ceil_div(T, rows_per_pass(E));
+  const int want = ceil_div(T, forward_threads_of(E) / lanes_of_row(E));
   return want < num_sms ? want : num_sms;
 }
 
@@ -350,12 +370,12 @@ moe_status router_losses_launch(const RouterLossArgs& a, cudaStream_t s) {
   const int blocks = forward_blocks(a.T > 0 ? a.T : 1, a.E, a.num_sms);
   MOE_TRY((dispatch<Forward, RouterLossArgs>(a.E, a, blocks, s)));
   if (blocks > 1)
-    MOE_TRY_CUDA(launch_k(router_losses_finalize_kernel, dim3(1), dim3(kThreads), 0, s, a, blocks));
+    MOE_TRY_CUDA(launch_k(router_losses_sum_kernel, dim3(kSumCtas), dim3(kSumThreads), 0, s, a, blocks));
   return MOE_OK;
 }
 
 moe_status router_losses_backward_launch(const RouterLossGradArgs& a, cudaStream_t s) {
-  const int want = ceil_div(a.T, rows_per_pass(a.E)), most = 4 * a.num_sms;
+  const int want = ceil_div(a.T, kThreads / lanes_of_row(a.E)), most = 6 * a.num_sms;
   return dispatch<Backward, RouterLossGradArgs>(a.E, a, want < most ? want : most, s);
 }
 

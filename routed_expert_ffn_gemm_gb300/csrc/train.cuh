@@ -27,20 +27,35 @@ struct BlockScale {
   float r;  // what values are multiplied by before rounding to E4M3
 };
 
-// Scale of a block from the bits of its largest finite magnitude.
-//   amax: s = a / 448, r = 448 / a, each correctly rounded;
-//   pow2: s = 2^p with a / 2^p in (224, 448], r = 2^-p exactly.
-template <bool POW2>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+// Scale of a block from the bits of its largest finite magnitude a: s = 2^p
+// with a / 2^p in (224, 448], r = 2^-p exactly.
+__device__ __forceinline__ BlockScale pow2_scale(uint32_t amax_bits) {
+  const uint32_t b = max(amax_bits, kMinAmaxBits);
+  // a = 1.m * 2^(E - 127); p = E - 135 while 1.m <= 1.75, else E - 134
+  const uint32_t e = (b >> 23) + ((b & 0x7fffffu) > 0x600000u ? 1u : 0u);
   if (amax_bits == 0u) return {1.f, 1.f};
-  const uint32_t b = amax_bits < kMinAmaxBits ? kMinAmaxBits : amax_bits;
-  if (POW2) {
-    // a = 1.m * 2^(E - 127); p = E - 135 while 1.m <= 1.75, else E - 134
-    const uint32_t e = (b >> 23) + ((b & 0x7fffffu) > 0x600000u ? 1u : 0u);
-    return {__uint_as_float((e - 8u) << 23), __uint_as_float((262u - e) << 23)};
+  return {__uint_as_float((e - 8u) << 23), __uint_as_float((262u - e) << 23)};
+}
+
+// s = a / 448 and r = 448 / a, each correctly rounded, for the blocks that
+// the 16 lanes hold (N of them, each amax known to all lanes): a lane does
+// one of the 2 N divisions.  Every lane of the warp calls this.
+template <int N>
+__device__ __forceinline__ void amax_scales(const uint32_t (&amax_bits)[N], BlockScale (&out)[N]) {
+  constexpr int EACH = 16 / (2 * N);  // lanes that do the same division
+  const int which = (threadIdx.x & 15) / EACH;
+  float a = __uint_as_float(max(amax_bits[0], kMinAmaxBits));
+#pragma unroll
+  for (int i = 1; i < N; ++i)
+    if (which >= 2 * i) a = __uint_as_float(max(amax_bits[i], kMinAmaxBits));
+  const bool scale = (which & 1) == 0;
+  const float q = __fdiv_rn(scale ? a : 448.f, scale ? 448.f : a);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float s = __shfl_sync(0xffffffffu, q, 2 * i * EACH, 16);
+    const float r = __shfl_sync(0xffffffffu, q, (2 * i + 1) * EACH, 16);
+    out[i] = amax_bits[i] == 0u ? BlockScale{1.f, 1.f} : BlockScale{s, r};
   }
-  const float a = __uint_as_float(b);
-  return {__fdiv_rn(a, 448.f), __fdiv_rn(448.f, a)};
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -49,30 +64,54 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The largest magnitude of 8 values over the 16 lanes that hold a block, as
-// bits.  E4M3 has no infinity: infinities and NaN do not count toward the
-// maximum and become NaN here (and so in the codes).  Every lane of the warp
-// calls this.
-__device__ __forceinline__ uint32_t block_amax(float (&v)[8]) {
-  uint32_t m = 0u;
+// The largest magnitudes of N blocks over the 16 lanes that hold 8 values of
+// each, as bits.  E4M3 has no infinity: infinities and NaN do not count
+// toward the maximum and become NaN here (and so in the codes).  Every lane
+// of the warp calls this.
+template <int N>
+__device__ __forceinline__ void finite_amax(float (&v)[N][8], uint32_t (&m)[N]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // rare: some value is not finite
-    m = 0u;
+  for (int n = 0; n < N; ++n) {
+    m[n] = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t a = abs_bits(v[i]);
+      const uint32_t a = abs_bits(v[n][i]);
       if (a < 0x7f800000u)
-        m = max(m, a);
+        m[n] = max(m[n], a);
       else
-        v[i] = __uint_as_float(0x7fffffffu);
+        v[n][i] = __uint_as_float(0x7fffffffu);
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 8; o > 0; o >>= 1) m[n] = max(m[n], __shfl_xor_sync(0xffffffffu, m[n], o));
   }
-  return m;
+}
+template <int N>
+__device__ __forceinline__ void block_amax(float (&v)[N][8], uint32_t (&m)[N]) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    m[n] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[n] = max(m[n], abs_bits(v[n][i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m[n] = max(m[n], __shfl_xor_sync(0xffffffffu, m[n], o));
+    top = max(top, m[n]);
+  }
+  if (__any_sync(0xffffffffu, top >= 0x7f800000u)) finite_amax(v, m);  // rare: some value is not finite
+}
+// The same of two blocks of bf16 values (8 of each in a and b, as stored):
+// the maxima travel as the halves of one word.
+__device__ __forceinline__ void block_amax_bf16(const uint4& a, const uint4& b, float (&v)[2][8], uint32_t (&m)[2]) {
+  auto top = [](const uint4& q) {  // of the even and of the odd elements
+    return __vmaxu2(__vmaxu2(q.x & 0x7fff7fffu, q.y & 0x7fff7fffu), __vmaxu2(q.z & 0x7fff7fffu, q.w & 0x7fff7fffu));
+  };
+  const uint32_t ta = top(a), tb = top(b);
+  uint32_t t = __vmaxu2(__byte_perm(ta, tb, 0x5410), __byte_perm(ta, tb, 0x7632));  // a's low, b's high
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+  m[0] = t << 16;
+  m[1] = t & 0xffff0000u;
+  if (__any_sync(0xffffffffu, max(m[0], m[1]) >= 0x7f800000u)) finite_amax(v, m);
 }
 
 __device__ __forceinline__ uint2 block_codes(const float (&v)[8], float r) {
@@ -82,14 +121,19 @@ __device__ __forceinline__ uint2 block_codes(const float (&v)[8], float r) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// The two E4M3 codes in the low 16 bits as fp32 (exact).
+__device__ __forceinline__ float2 e4m3_pair_values(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // Eight E4M3 codes as fp32 (exact).
 __device__ __forceinline__ void e4m3_values(uint2 c, float (&v)[8]) {
   const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w[i]));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const float2 f = e4m3_pair_values(w[i]);
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
   }

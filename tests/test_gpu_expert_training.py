@@ -512,3 +512,22 @@ def test_operators_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip((*got, dw), want))
+
+
+def test_wgrad_multiplies_every_code_out():
+    # every E4M3 code under powers of two (small, large, at the edges of what
+    # one bf16 product covers) and other scales: dy picks single rows out, so
+    # each element is one code times its scale, rounded once to bf16
+    K, N = 256, 64
+    x = torch.arange(256, dtype=torch.uint8).repeat(N, 1)
+    scales = torch.tensor([[2.0 ** (7 - 4 * r), 1.3 * 2.0 ** (r - 40)] for r in range(N)])
+    scales[0], scales[1], scales[2] = torch.tensor([2.0 ** 8, 2.0 ** 100]), torch.tensor([2.0 ** -126, 0.0]), -0.5
+    dy = torch.eye(N).bfloat16()
+    dw = api.grouped_wgrad(dy.to(DEV), x.to(DEV), scales.to(DEV), offsets_of([N]).to(DEV)).cpu()[0]
+    s = scales.repeat_interleave(128, 1)
+    want = (ref.e4m3(x).float() * s).bfloat16().float()
+    # (a NaN code reaches every n of its column: 0 * NaN is NaN)
+    nan = torch.isnan(want).any(0)
+    assert torch.equal(nan, torch.tensor([c % 128 == 127 for c in range(256)]))
+    assert torch.isnan(dw[:, nan]).all()
+    assert torch.equal(dw[:, ~nan], want[:, ~nan])
