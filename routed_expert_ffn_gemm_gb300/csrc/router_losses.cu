@@ -109,11 +109,14 @@ __global__ void __launch_bounds__(THREADS) router_losses_kernel(const RouterLoss
 #pragma unroll
   for (int i = 0; i < NI * VEC; ++i) P[i] = 0.f;
   const int step = gridDim.x * WARPS * RPW;
-  for (int t0 = (blockIdx.x * WARPS + warp) * RPW; t0 < a.T; t0 += step) {
-    const int t = t0 + lane / LG;
+  int t = (blockIdx.x * WARPS + warp) * RPW + lane / LG;
+  Row<LG, VEC, NI> ahead;
+  if (t < a.T) ahead.load(a.logits + (size_t)t * a.E, a.E, l);
+  // (all rows of the warp take the same number of steps)
+  for (int t0 = t - lane / LG; t0 < a.T; t0 += step, t += step) {
     const bool here = t < a.T, live = here && (a.mask == nullptr || a.mask[t] != 0);
-    Row<LG, VEC, NI> r;
-    if (here) r.load(a.logits + (size_t)t * a.E, a.E, l);
+    Row<LG, VEC, NI> r = ahead;  // the next row is on its way during this one
+    if (t + step < a.T) ahead.load(a.logits + (size_t)(t + step) * a.E, a.E, l);
     if (live)
       for (int j = l; j < a.k; j += LG) {
         const int e = a.idx[(size_t)t * a.k + j];
@@ -180,34 +183,47 @@ __global__ void __launch_bounds__(THREADS) router_losses_kernel(const RouterLoss
   }
 }
 
-// Sums the parts in a fixed order: one cluster, its CTAs taking E / 8 experts
-// each, 32 threads an expert; the first CTA adds their shares of
-// sum_e c_e P_e through distributed shared memory.
+// Sums the parts in a fixed order: one cluster, its CTAs taking 32 experts at
+// a time, a warp every 32nd part of them; the first CTA adds the CTAs' shares
+// of sum_e c_e P_e through distributed shared memory.
 __global__ void __launch_bounds__(kSumThreads) __cluster_dims__(kSumCtas, 1, 1)
     router_losses_sum_kernel(const RouterLossArgs a, int nparts) {
   griddep_begin();
-  __shared__ float red[kSumThreads / 32];
-  __shared__ int red_n[kSumThreads / 32];
+  constexpr int WARPS = kSumThreads / 32;
+  __shared__ float sum_p[WARPS][32], red[WARPS];
+  __shared__ int sum_c[WARPS][32], red_n[WARPS];
   __shared__ float shares[kSumCtas];
   const uint32_t* parts = static_cast<const uint32_t*>(a.workspace);
   const size_t pw = part_words(a.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x;
   float dot = 0.f;
-  for (int e = rank * (kSumThreads / 32) + warp; e < a.E; e += kSumCtas * (kSumThreads / 32)) {
+  for (int e0 = rank * 32; e0 < a.E; e0 += kSumCtas * 32) {
+    const int e = e0 + lane;
     float P = 0.f;
     int c = 0;
-    for (int b = lane; b < nparts; b += 32) {
-      P += __uint_as_float(__ldcg(parts + b * pw + e));
-      c += (int)__ldcg(parts + b * pw + a.E + e);
-    }
-    P = warp_sum(P);
-    c = warp_sum(c);
-    if (lane == 0) {
+    if (e < a.E)
+#pragma unroll 5
+      for (int b = warp; b < nparts; b += WARPS) {
+        P += __uint_as_float(__ldcg(parts + b * pw + e));
+        c += (int)__ldcg(parts + b * pw + a.E + e);
+      }
+    sum_p[warp][lane] = P;
+    sum_c[warp][lane] = c;
+    __syncthreads();
+    if (warp == 0 && e < a.E) {
+      P = 0.f;
+      c = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        P += sum_p[w][lane];
+        c += sum_c[w][lane];
+      }
       a.counts[e] = c;
       dot += (float)c * P;
     }
+    __syncthreads();
   }
-  dot = block_sum(dot, red);
+  dot = warp_sum(dot);  // (warp 0 has them all)
   float zs = 0.f;
   int n = 0;
   if (rank == 0) {
@@ -248,29 +264,48 @@ __global__ void __launch_bounds__(kThreads) router_losses_backward_kernel(const 
   const float up = (a.grad != nullptr ? *a.grad : 1.f) * inv_n;
   const float cb = a.balance * (float)a.E, cz = 2.f * a.z;
   const int step = gridDim.x * kWarps * RPW;
-  for (int t0 = (blockIdx.x * kWarps + warp) * RPW; t0 < a.T; t0 += step) {
-    const int t = t0 + lane / LG;
-    const bool here = t < a.T, live = here && (a.mask == nullptr || a.mask[t] != 0);
+  int t = (blockIdx.x * kWarps + warp) * RPW + lane / LG;
+  constexpr int KI = 32 / LG;  // most kept slots of a lane
+  struct Ahead {
     Row<LG, VEC, NI> r;
-    float lse = -INFINITY;
-    if (here) {
-      r.load(a.logits + (size_t)t * a.E, a.E, l);
-      lse = a.lse[t];
-    }
+    float lse, w[KI], dw[KI];
+    int e[KI];
+  } ahead;
+  auto load = [&](int t) {
+    if (t >= a.T) return;
+    ahead.r.load(a.logits + (size_t)t * a.E, a.E, l);
+    ahead.lse = a.lse[t];
+    if (a.w != nullptr)
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        const int j = l + i * LG;
+        const size_t at = (size_t)t * a.k + j;
+        ahead.w[i] = j < a.k ? a.w[at] : 0.f;
+        ahead.dw[i] = j < a.k ? a.dw[at] : 0.f;
+        ahead.e[i] = j < a.k ? a.idx[at] : -1;
+      }
+  };
+  load(t);
+  for (int t0 = t - lane / LG; t0 < a.T; t0 += step, t += step) {
+    const bool here = t < a.T, live = here && (a.mask == nullptr || a.mask[t] != 0);
+    Ahead now = ahead;  // the next row is on its way during this one
+    load(t + step);
+    Row<LG, VEC, NI>& r = now.r;
+    const float lse = here ? now.lse : -INFINITY;
     if (a.w != nullptr) {
       float dot = 0.f;
-      if (here)
-        for (int j = l; j < a.k; j += LG) dot = fmaf(a.w[(size_t)t * a.k + j], a.dw[(size_t)t * a.k + j], dot);
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+        if (here) dot = fmaf(now.w[i], now.dw[i], dot);
       dot = group_sum<LG>(dot);
-      if (here)
-        for (int j = l; j < a.k; j += LG) {
-          const size_t at = (size_t)t * a.k + j;
-          const int e = a.idx[at];
-          if (e >= 0 && e < a.E)
-            atomicAdd(add + e, a.w[at] * (a.dw[at] - dot));  // (distinct experts: one add each)
-          else
-            set_device_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-        }
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        const int e = here ? now.e[i] : -1;
+        if (e >= 0 && e < a.E)
+          atomicAdd(add + e, now.w[i] * (now.dw[i] - dot));  // (distinct experts: one add each)
+        else if (here && l + i * LG < a.k)
+          set_device_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      }
       __syncwarp();
     }
     const bool some = live && lse != -INFINITY;
@@ -301,11 +336,9 @@ __global__ void __launch_bounds__(kThreads) router_losses_backward_kernel(const 
     }
     if (a.w != nullptr) {
       __syncwarp();
-      if (here)
-        for (int j = l; j < a.k; j += LG) {
-          const int e = a.idx[(size_t)t * a.k + j];
-          if (e >= 0 && e < a.E) add[e] = 0.f;
-        }
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+        if (here && now.e[i] >= 0 && now.e[i] < a.E) add[now.e[i]] = 0.f;
       __syncwarp();
     }
   }
@@ -375,7 +408,7 @@ moe_status router_losses_launch(const RouterLossArgs& a, cudaStream_t s) {
 }
 
 moe_status router_losses_backward_launch(const RouterLossGradArgs& a, cudaStream_t s) {
-  const int want = ceil_div(a.T, kThreads / lanes_of_row(a.E)), most = 6 * a.num_sms;
+  const int want = ceil_div(a.T, kThreads / lanes_of_row(a.E)), most = 4 * a.num_sms;
   return dispatch<Backward, RouterLossGradArgs>(a.E, a, want < most ? want : most, s);
 }
 
