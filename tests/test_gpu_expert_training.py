@@ -531,3 +531,19 @@ def test_wgrad_multiplies_every_code_out():
     assert torch.equal(nan, torch.tensor([c % 128 == 127 for c in range(256)]))
     assert torch.isnan(dw[:, nan]).all()
     assert torch.equal(dw[:, ~nan], want[:, ~nan])
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["forward", "gradient"])
+@pytest.mark.parametrize("K", [128, 384, 656])
+def test_block_gemm_tiles_of_every_size_in_turn(K, transposed):
+    # tiles with many rows and with few alternate on every CTA, so that the
+    # accumulators change hands again and again; blocks in no multiple of four
+    counts = [[300, 5, 97, 40, 96, 256, 1, 130, 70, 33, 0, 512, 64][i % 13] for i in range(130)]
+    N = 512
+    R, a, sa, off, w, sw = gemm_case(counts, 0, 0, K, N, transposed, seed=K)
+    args = [t.to(DEV) for t in (a, sa, off, w, sw)]
+    got = api.grouped_block_gemm(*args, transposed, out_dtype=torch.float32)
+    for _ in range(20):
+        assert torch.equal(api.grouped_block_gemm(*args, transposed, out_dtype=torch.float32), got)
+    y, mag = ref.block_gemm(a, sa, off, w, sw, transposed)
+    assert ((got.cpu().double() - y).abs() <= (32 + 4 * ref.blocks(K)) * U * mag).all()
