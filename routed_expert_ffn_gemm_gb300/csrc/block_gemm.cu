@@ -40,35 +40,43 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kBN = 256;                      // most rows of a unit
-constexpr int kStages = 4;                    // slots; block j of a step of four takes slot j
 constexpr int kOwnBytes = 128 * 128;          // the CTA's own operand (M side): 128 rows of 128 codes
-constexpr int kStageBytes = kOwnBytes + 256 * 128;  // and the shared one (N side)
-constexpr int kGroup = 4, kScaleRing = 2;  // blocks of a step: slot j holds block j; scale groups in flight
+constexpr int kGroup = 4, kScaleRing = 2;     // blocks of a step; steps' scales in flight
 constexpr int kEpiWarps = 8;
 constexpr int kBand = 16;                     // row tiles that share a pass over the weights
-constexpr int kChunks = 4;                    // chunks of 32 rows of an accumulating warp
+constexpr int kChunks = 4;                    // chunks of 32 columns of an accumulating warp
 constexpr int kOutPitch = 36;                 // words of a staged pair of rows (32 channels), padded against conflicts
-// From this many rows on a unit's rows are the MMA's M side (always 256 of
-// them), below it the N side (a multiple of 32): see the head of the file.
-constexpr int kRowsOnM = 97;
 constexpr int kOutBytes = 2048;               // staging of an accumulating warp: 32 rows of 64 bytes
 static_assert(8 * 4 * kOutPitch <= kOutBytes, "staged pairs of rows");
 constexpr int kMaxGroups = 1024;
-constexpr int kOutOff = kStages * kStageBytes;
-constexpr int kScaleOff = kOutOff + kEpiWarps * kOutBytes;
-constexpr int kWScaleOff = kScaleOff + kScaleRing * kGroup * kBN * 4;  // [ring][group][channel half]
-constexpr int kBarOff = kWScaleOff + kScaleRing * kGroup * 8;
-// full[S], empty[S], acc_full[2], acc_empty[2], scale_full[2], scale_empty[2], drain
-constexpr int kNumBars = 2 * kStages + 4 + 2 * kScaleRing + 1;
-constexpr int kSlotOff = kBarOff + 8 * kNumBars;
-constexpr int kAbortOff = kSlotOff + 8;
-constexpr int kOffsOff = kAbortOff + 8;
-constexpr int kPrefixOff = kOffsOff + 4 * (kMaxGroups + 4);
-constexpr int kSmemBytes = kPrefixOff + 4 * (kMaxGroups + 4) + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
-// every CTA holds all of its SM's tensor memory: never two on one SM
-static_assert(2 * (kSmemBytes + 1024) > 232448 + 1024, "one CTA per SM");
+
+// Tiles of up to 256 rows, or (FEW) 64: with few rows an expert, weights are
+// all that moves, and slots of 24 KB instead of 48 keep twice as many of them
+// in flight (8 rows of one token, 7168 x 4096: 53 -> 47 us).
+template <bool FEW>
+struct Tile {
+  static constexpr int ROWS = FEW ? 64 : 256;
+  static constexpr int STEPS = FEW ? 2 : 1;               // steps in flight: block j of step i takes slot 4 (i % STEPS) + j
+  static constexpr int STAGES = kGroup * STEPS;
+  static constexpr int STAGE_BYTES = kOwnBytes + ROWS * 128;  // and the shared operand (N side)
+  static constexpr int OUT_OFF = STAGES * STAGE_BYTES;
+  static constexpr int SCALE_OFF = OUT_OFF + kEpiWarps * kOutBytes;
+  static constexpr int WSCALE_OFF = SCALE_OFF + kScaleRing * kGroup * ROWS * 4;  // [ring][block][channel half]
+  static constexpr int BAR_OFF = WSCALE_OFF + kScaleRing * kGroup * 8;
+  // full[S], empty[S], acc_full[2], acc_empty[2], scale_full[2], scale_empty[2], drain
+  static constexpr int NUM_BARS = 2 * STAGES + 4 + 2 * kScaleRing + 1;
+  static constexpr int SLOT_OFF = BAR_OFF + 8 * NUM_BARS;
+  static constexpr int ABORT_OFF = SLOT_OFF + 8;
+  static constexpr int OFFS_OFF = ABORT_OFF + 8;
+  static constexpr int PREFIX_OFF = OFFS_OFF + 4 * (kMaxGroups + 4);
+  static constexpr int SMEM_BYTES = PREFIX_OFF + 4 * (kMaxGroups + 4) + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  // every CTA holds all of its SM's tensor memory: never two on one SM
+  static_assert(2 * (SMEM_BYTES + 1024) > 232448 + 1024, "one CTA per SM");
+};
+// From this many rows on a unit's rows are the MMA's M side (always 256 of
+// them), below it the N side (a multiple of 32): see the head of the file.
+constexpr int kRowsOnM = 97;
 // Registers: 384 x 168 at launch; the accumulating warps take what the
 // other warpgroup gives back.
 constexpr int kRegsLow = 72, kRegsHigh = 216;
@@ -97,7 +105,9 @@ struct Unit {
   bool rows_m;
 };
 
+template <bool FEW>
 __device__ __forceinline__ Unit unit_of(int u, const int* offs, const int* prefix, int E, int MT) {
+  constexpr int ROWS = Tile<FEW>::ROWS;
   const int t = u / MT;
   int lo = 0, hi = E - 1;  // the expert whose tiles hold t
   while (lo < hi) {
@@ -112,12 +122,12 @@ __device__ __forceinline__ Unit unit_of(int u, const int* offs, const int* prefi
   const int wide = min(kBand, x.tiles - band * kBand);
   x.mt = rem / wide;
   const int rt = band * kBand + rem % wide;
-  const int r0 = rt * kBN;
+  const int r0 = rt * ROWS;
   x.row0 = offs[lo] + r0;
-  x.n_valid = min(kBN, offs[lo + 1] - x.row0);
-  x.rows_m = x.n_valid >= kRowsOnM;
-  x.n_mma = x.rows_m ? kBN : (x.n_valid + 31) / 32 * 32;  // (two boxes of at least 16)
-  x.batch = x.rows_m ? 1 : x.n_mma <= 64 ? 4 : 2;
+  x.n_valid = min(ROWS, offs[lo + 1] - x.row0);
+  x.rows_m = !FEW && x.n_valid >= kRowsOnM;
+  x.n_mma = x.rows_m ? ROWS : (x.n_valid + 31) / 32 * 32;  // (two boxes of at least 16)
+  x.batch = x.rows_m ? 1 : FEW || x.n_mma <= 64 ? 4 : 2;
   return x;
 }
 
@@ -157,7 +167,7 @@ struct Accumulate {
 
   // Rows on N: n of BATCH blocks of 256 / BATCH columns; a column's scale is
   // its row's times the block's for the CTA's channels.
-  template <int BATCH>
+  template <int BATCH, int ROWS>
   __device__ __forceinline__ void rows_n(float (&acc)[kChunks][32], uint32_t buf, int n, int n_mma, const float* sc,
                                          const float* ws) const {
     constexpr int PER = 4 / BATCH;  // chunks of this warp in a block
@@ -169,7 +179,7 @@ struct Accumulate {
         ptx::tmem_ld32(at + 256u * buf + 64u * t, d);
         ptx::tmem_ld_wait();
         const float w = ws[2 * (t / PER)];
-        const float* s = sc + (t / PER) * kBN + (t % PER) * 64 + first;
+        const float* s = sc + (t / PER) * ROWS + (t % PER) * 64 + first;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const float4 s4 = *reinterpret_cast<const float4*>(s + j);
@@ -293,13 +303,15 @@ __device__ __forceinline__ void store_rows_m(const Params& p, const CUtensorMap*
   }
 }
 
-template <bool TRANS>
+template <bool TRANS, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p, const __grid_constant__ Maps maps) {
+  using T = Tile<FEW>;
+  constexpr int kBN = T::ROWS, kStages = T::STAGES, kStageBytes = T::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = ptx::smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
-  const uint32_t sbase = raw_s + pad, bars = sbase + kBarOff;
+  const uint32_t sbase = raw_s + pad, bars = sbase + T::BAR_OFF;
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (kStages + s); };
   auto accf_bar = [&](int b) { return bars + 8u * (2 * kStages + b); };
@@ -307,12 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
   auto sfull_bar = [&](int i) { return bars + 8u * (2 * kStages + 4 + i); };
   auto sempty_bar = [&](int i) { return bars + 8u * (2 * kStages + 4 + kScaleRing + i); };
   const uint32_t drain_bar = bars + 8u * (2 * kStages + 4 + 2 * kScaleRing);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOff);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
-  int* offs = reinterpret_cast<int*>(smem + kOffsOff);
-  int* prefix = reinterpret_cast<int*>(smem + kPrefixOff);
-  float* scales = reinterpret_cast<float*>(smem + kScaleOff);
-  float* wscales = reinterpret_cast<float*>(smem + kWScaleOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::SLOT_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::ABORT_OFF);
+  int* offs = reinterpret_cast<int*>(smem + T::OFFS_OFF);
+  int* prefix = reinterpret_cast<int*>(smem + T::PREFIX_OFF);
+  float* scales = reinterpret_cast<float*>(smem + T::SCALE_OFF);
+  float* wscales = reinterpret_cast<float*>(smem + T::WSCALE_OFF);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
@@ -386,9 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
       // ---------------------------------------------------------- copies
       const uint64_t once = ptx::policy_evict_first(), keep = ptx::policy_evict_normal();
       uint32_t used = 0;  // bit j: parity of slot j's uses
+      int base = 0;       // the step's first slot
       bool ok = true;
       for (int u = u_first; u < units && ok; u += u_step) {
-        const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
+        const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
         // shared rows come in two boxes of 16, 32, 64 or 128 rows, one from each CTA
         const int half = x.n_mma / 2;
         const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
@@ -399,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
         const int ch = x.mt * 256 + (int)rank * 128, row = x.row0 + (int)rank * (16 << box);
         const uint64_t pol = x.tiles > 1 ? keep : once;
         for (int kb = 0; kb < p.KB; ++kb) {
-          const int stage = kb % kStages;
+          const int stage = base + kb % kGroup;
           if (!ptx::mbar_wait_bounded(empty_bar(stage), ((used >> stage) & 1u) ^ 1u, deadline, abort_flag)) {
             ok = false;
             break;
@@ -415,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
             ptx::tma_load_2d_cast(sa + r_at, am, fb, kb * 128, row, 3, keep);
           }
           used ^= 1u << stage;
+          if (kb % kGroup == kGroup - 1 || kb == p.KB - 1) base = (base + kGroup) % kStages;
         }
       }
       if (!ok) {
@@ -434,9 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
       const uint32_t one = ptx::elect_one() ? 1u : 0u;
       uint32_t slots = 0, bufs = 0;  // bit j: parity of the uses of slot j, of buffer j
       uint32_t next = 0;             // the buffer of a step of four blocks that share one
+      int base = 0;                  // the step's first slot
       bool ok = true, any = false;
       for (int u = u_first; u < units && ok; u += u_step) {
-        const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
+        const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
         const int n_mma = __shfl_sync(0xffffffffu, x.n_mma, 0), batch = __shfl_sync(0xffffffffu, x.batch, 0);
         const bool rows_m = batch == 1;
         const uint32_t idesc =
@@ -449,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
         // for 2, 3, or one for all four.  A poll takes some 70 cycles, so the
         // next block's barriers are asked while this block's MMAs run.
         auto buffer = [&](int j) { return batch == 1 ? (uint32_t)(j & 1) : batch == 2 ? (uint32_t)(j >> 1) : next; };
-        auto polled = [&](int j) {
-          const bool f = ptx::mbar_test_wait(full_bar(j), (slots >> j) & 1u);
+        auto polled = [&](int from, int j) {
+          const bool f = ptx::mbar_test_wait(full_bar(from + j), (slots >> (from + j)) & 1u);
           if (j & (batch - 1)) return f;
           const uint32_t b = buffer(j);
           return ptx::mbar_test_wait(acce_bar(b), ((bufs >> b) & 1u) ^ 1u) && f;
@@ -463,32 +478,35 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
           for (int j = 0; j < kGroup; ++j) {
             if (j >= n || !ok) break;
             const uint32_t b = buffer(j);
+            const int slot = base + j;
             if (!seen) {
-              ok = ptx::mbar_wait_bounded(full_bar(j), (slots >> j) & 1u, deadline, abort_flag) &&
+              ok = ptx::mbar_wait_bounded(full_bar(slot), (slots >> slot) & 1u, deadline, abort_flag) &&
                    ((j & (batch - 1)) != 0 ||
                     ptx::mbar_wait_bounded(acce_bar(b), ((bufs >> b) & 1u) ^ 1u, deadline, abort_flag));
             }
             ok = __all_sync(0xffffffffu, ok) != 0;
             if (!ok) break;
             ptx::tc_fence_after();
-            slots ^= 1u << j;
+            slots ^= 1u << slot;
             const bool last = (j & (batch - 1)) == batch - 1 || j == n - 1;
             if (last) {
               bufs ^= 1u << b;
               next ^= batch == 4 ? 1u : 0u;
             }
             const uint32_t d = tmem_base + 256u * b + (uint32_t)((j & (batch - 1)) * cols);
-            const uint64_t da = da0 + (uint32_t)(j * (kStageBytes >> 4)), db = db0 + (uint32_t)(j * (kStageBytes >> 4));
+            const uint64_t da = da0 + (uint32_t)(slot * (kStageBytes >> 4)),
+                           db = db0 + (uint32_t)(slot * (kStageBytes >> 4));
             ptx::mma_f8_one<false>(one, d, da, db, idesc);  // 32 of the block's 128 per instruction
             ptx::mma_f8_one<true>(one, d, da + astep, db + bstep, idesc);
             ptx::mma_f8_one<true>(one, d, da + 2 * astep, db + 2 * bstep, idesc);
             ptx::mma_f8_one<true>(one, d, da + 3 * astep, db + 3 * bstep, idesc);
             if (last) ptx::mma_commit_one(one, accf_bar(b));
-            ptx::mma_commit_cast_one(one, empty_bar(j), 3);
+            ptx::mma_commit_cast_one(one, empty_bar(slot), 3);
             // (only within the unit: the next one may use the buffers in another way)
-            seen = j + 1 < n ? polled(j + 1) : kb0 + kGroup < p.KB && polled(0);
+            seen = j + 1 < n ? polled(base, j + 1) : kb0 + kGroup < p.KB && polled((base + kGroup) % kStages, 0);
             any = true;
           }
+          base = (base + kGroup) % kStages;
         }
       }
       if (!ok && one) {
@@ -506,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
       uint32_t it = 0;
       bool ok = true;
       for (int u = u_first; u < units && ok; u += u_step) {
-        const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
+        const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
         // rows on N: all rows, this CTA's 128 channels; rows on M: this CTA's
         // 128 rows, both halves of the channels.  (Channels past N: zero
         // weights, never stored.)
@@ -521,14 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
             ok = false;
             break;
           }
-          const uint32_t to = sbase + kScaleOff + slot * (kGroup * kBN * 4) + lane * 4;
+          const uint32_t to = sbase + T::SCALE_OFF + slot * (kGroup * kBN * 4) + lane * 4;
           const int n = min(kGroup, p.KB - kb);
           for (int r = lane; r < rows; r += 32)
 #pragma unroll
             for (int j = 0; j < kGroup; ++j)
               if (j < n) ptx::cp_async4(to + (uint32_t)(j * kBN + r - lane) * 4, ap + (size_t)(r - lane) * p.KB + kb + j);
           if ((lane >> 1) < n)  // lane: block lane / 2, channel half lane & 1
-            ptx::cp_async4(sbase + kWScaleOff + slot * (kGroup * 8) + lane * 4,
+            ptx::cp_async4(sbase + T::WSCALE_OFF + slot * (kGroup * 8) + lane * 4,
                            wp + (size_t)(kb + (lane >> 1)) * (TRANS ? p.NB : 1));
           ptx::cp_async_arrive_noinc(sfull_bar(slot));
         }
@@ -540,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
     // ------------------------------------------------------- accumulation
     ptx::regs_inc<kRegsHigh>();
     const int q = warp & 3, eg = (warp - 4) >> 2;
-    uint8_t* outb = smem + kOutOff + (warp - 4) * kOutBytes;
+    uint8_t* outb = smem + T::OUT_OFF + (warp - 4) * kOutBytes;
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
     const Accumulate step{tlane + eg * 32, eg * 32, q * 32 + lane};
     uint32_t sit = 0, bufs = 0, next = 0;  // (bufs, next: as the MMA warp has them)
@@ -548,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
     for (int u = u_first; u < units; u += u_step) {
       int n_mma, batch;
       {
-        const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
+        const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
         n_mma = x.n_mma;
         batch = x.batch;
       }
@@ -576,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
           if (lane == 0) ptx::mbar_arrive(acce_bar(b));
           bufs ^= 1u << b;
         };
-        if (batch == 1) {
+        if (!FEW && batch == 1) {
           bool seen = arrived(0);
 #pragma unroll 1
           for (int j = 0; j < n; ++j) {
@@ -589,18 +607,18 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
               seen = arrived(b ^ 1u);  // (the answer comes while the last columns are added)
             });
           }
-        } else if (batch == 2) {
+        } else if (!FEW && batch == 2) {
           for (int j = 0; j < n; j += 2) {
             const uint32_t b = j >> 1;
             ok = acquire(b, arrived(b));
             if (!ok) break;
-            step.rows_n<2>(acc, b, min(2, n - j), n_mma, sc + j * kBN, ws + 2 * j);
+            step.template rows_n<2, kBN>(acc, b, min(2, n - j), n_mma, sc + j * kBN, ws + 2 * j);
             release(b);
           }
         } else {
           ok = acquire(next, arrived(next));
           if (ok) {
-            step.rows_n<4>(acc, next, n, n_mma, sc, ws);
+            step.template rows_n<4, kBN>(acc, next, n, n_mma, sc, ws);
             release(next);
             next ^= 1u;
           }
@@ -611,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
       }
       if (!ok) break;
       // (worked out again: the registers hold sums during the loop)
-      const Unit x = unit_of(u, offs, prefix, p.E, p.MT);
-      if (x.rows_m)
+      const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
+      if (!FEW && x.rows_m)
         store_rows_m(p, &maps.out, x, acc, (int)rank * 128 + q * 32, x.mt * 256 + eg * 32, outb);
       else
         store_rows_n(p, x, acc, x.mt * 256 + (int)rank * 128 + q * 32, eg * 32, outb);
@@ -632,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
 
 // CTAs (two per pair) that are resident at once: the grid is persistent and
 // not every SM finds a partner.  One value per device, written once.
-template <bool TRANS>
+template <bool TRANS, bool FEW>
 moe_status resident_ctas(int* out) {
   static std::atomic<int> known[64];
   int dev = 0;
@@ -640,12 +658,12 @@ moe_status resident_ctas(int* out) {
   if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
   int n = known[dev].load(std::memory_order_relaxed);
   if (n == 0) {
-    auto kern = block_gemm_kernel<TRANS>;
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+    auto kern = block_gemm_kernel<TRANS, FEW>;
+    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<FEW>::SMEM_BYTES));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = Tile<FEW>::SMEM_BYTES;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -661,16 +679,16 @@ moe_status resident_ctas(int* out) {
   return MOE_OK;
 }
 
-template <bool TRANS>
+template <bool TRANS, bool FEW>
 moe_status launch(const Params& p, const Maps& maps, int num_sms, cudaStream_t s) {
   int ctas = 0;
-  MOE_TRY(resident_ctas<TRANS>(&ctas));
-  // no more pairs than units can exist: row tiles <= R / 256 + one per group
-  const long long tiles = (long long)p.R / kBN + (p.R < p.E ? p.R : p.E);
+  MOE_TRY((resident_ctas<TRANS, FEW>(&ctas)));
+  // no more pairs than units can exist: whole row tiles, and one per group
+  const long long tiles = (long long)p.R / Tile<FEW>::ROWS + (p.R < p.E ? p.R : p.E);
   const long long units = tiles * p.MT;
   int grid = ctas < num_sms ? ctas : num_sms & ~1;
   if (2 * units < grid) grid = (int)(2 * units);
-  MOE_TRY_CUDA(launch_kc(2, block_gemm_kernel<TRANS>, dim3(grid), dim3(kThreads), kSmemBytes, s, p, maps));
+  MOE_TRY_CUDA(launch_kc(2, block_gemm_kernel<TRANS, FEW>, dim3(grid), dim3(kThreads), Tile<FEW>::SMEM_BYTES, s, p, maps));
   return MOE_OK;
 }
 
@@ -692,7 +710,7 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
   p.out = a.out;
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;
-  if (((long long)a.R / kBN + a.E) * p.MT > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  if (((long long)a.R / Tile<true>::ROWS + a.E) * p.MT > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
   Maps maps;
   if (a.transposed)
     MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.K, a.N, a.N, 1, 128, 128, 128));
@@ -701,7 +719,11 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
   for (int i = 0; i < 4; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K, 1, 16u << i, 128, 128));
   const int es = a.out_f32 ? 4 : 2;
   MOE_TRY(make_tmap_2d(&maps.out, a.out, a.R, a.N, es, 32, 64 / es, 64));
-  return a.transposed ? launch<true>(p, maps, a.num_sms, s) : launch<false>(p, maps, a.num_sms, s);
+  // Few rows an expert on average (a group of more than 64 rows then takes
+  // several tiles, whose weights come from L2 again).
+  const bool few = a.R <= 64 || (long long)a.R <= 16ll * a.E;
+  if (few) return a.transposed ? launch<true, true>(p, maps, a.num_sms, s) : launch<false, true>(p, maps, a.num_sms, s);
+  return a.transposed ? launch<true, false>(p, maps, a.num_sms, s) : launch<false, false>(p, maps, a.num_sms, s);
 }
 
 }  // namespace moe
