@@ -52,7 +52,8 @@ constexpr int kMaxGroups = 1024;
 
 // Tiles of up to 256 rows, or (FEW) 64: with few rows an expert, weights are
 // all that moves, and slots of 24 KB instead of 48 keep twice as many of them
-// in flight (8 rows of one token, 7168 x 4096: 53 -> 47 us).
+// in flight (8 rows of one token, 7168 x 4096: 53 -> 46 us; 512 rows of 230
+// experts of 2048 x 7168: 565 -> 477).
 template <bool FEW>
 struct Tile {
   static constexpr int ROWS = FEW ? 64 : 256;
@@ -75,8 +76,10 @@ struct Tile {
   static_assert(2 * (SMEM_BYTES + 1024) > 232448 + 1024, "one CTA per SM");
 };
 // From this many rows on a unit's rows are the MMA's M side (always 256 of
-// them), below it the N side (a multiple of 32): see the head of the file.
-constexpr int kRowsOnM = 97;
+// them), below it the N side (a multiple of 32): see the head of the file.  64
+// experts of 7168 x 4096 with 120 rows each took 404 us on N and 438 on M;
+// 80 rows 375 and 434.
+constexpr int kRowsOnM = 129;
 // Registers: 384 x 168 at launch; the accumulating warps take what the
 // other warpgroup gives back.
 constexpr int kRegsLow = 72, kRegsHigh = 216;
@@ -720,8 +723,9 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
   const int es = a.out_f32 ? 4 : 2;
   MOE_TRY(make_tmap_2d(&maps.out, a.out, a.R, a.N, es, 32, 64 / es, 64));
   // Few rows an expert on average (a group of more than 64 rows then takes
-  // several tiles, whose weights come from L2 again).
-  const bool few = a.R <= 64 || (long long)a.R <= 16ll * a.E;
+  // several tiles, whose weights come from L2 again).  64 experts of 7168 x
+  // 4096 with 40 rows each: 303 us in tiles of 64, 349 in tiles of 256.
+  const bool few = a.R <= 64 || (long long)a.R <= 48ll * a.E;
   if (few) return a.transposed ? launch<true, true>(p, maps, a.num_sms, s) : launch<false, true>(p, maps, a.num_sms, s);
   return a.transposed ? launch<true, false>(p, maps, a.num_sms, s) : launch<false, false>(p, maps, a.num_sms, s);
 }
