@@ -42,14 +42,14 @@ constexpr int kCodeBytes = kRows * 128;
 constexpr int kEpiWarps = 8, kPrepWarps = 4;
 constexpr int kBand = 8;
 constexpr int kMaxGroups = 1024;
-constexpr int kOutBytes = 32 * 64;            // per accumulating warp: 32 rows of 64 bytes
+constexpr int kOutBufs = 2, kOutBytes = 32 * 64;  // per accumulating warp: staged boxes of 32 rows of 64 bytes
 
 template <bool CODES>
 struct Smem {
-  static constexpr int STAGES = CODES ? 5 : 6;
+  static constexpr int STAGES = CODES ? 4 : 5;
   static constexpr int STAGE_BYTES = 2 * kTileBytes + (CODES ? kCodeBytes : 0);
   static constexpr int OUT_OFF = STAGES * STAGE_BYTES;
-  static constexpr int BAR_OFF = OUT_OFF + kEpiWarps * kOutBytes;
+  static constexpr int BAR_OFF = OUT_OFF + kEpiWarps * kOutBufs * kOutBytes;
   // full[S], ready[S], empty[S], acc_full[2], acc_empty[2], drain
   static constexpr int NUM_BARS = 3 * STAGES + 5;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NUM_BARS + 8;
@@ -347,10 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
     // ------------------------------------------------------- accumulation
     ptx::regs_inc<kRegsHigh>();
     const int q = warp & 3, eg = (warp - 8) >> 2;
-    uint8_t* outb = smem + S::OUT_OFF + (warp - 8) * kOutBytes;
+    uint8_t* outb = smem + S::OUT_OFF + (warp - 8) * kOutBufs * kOutBytes;
     const uint32_t out_s = ptx::smem_u32(outb);
     const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
-    uint32_t it = 0;
+    uint32_t it = 0, boxes = 0;
     bool ok = true;
     for (int u = u_first; u < units; u += u_step) {
       const Unit x = unit_of(u, offs, p);
@@ -400,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
           if (h == 1 && !p.out_f32) break;
           const int k0 = x.kt * 256 + (2 * i + eg) * 32 + h * per;
           if (k0 >= p.K) break;
-          if (lane == 0) ptx::bulk_wait_read<0>();  // the previous box has left the buffer
+          if (lane == 0) ptx::bulk_wait_read<kOutBufs - 1>();  // the box before the last has left its buffer
           __syncwarp();
+          const uint32_t ob = (uint32_t)(boxes++ % kOutBufs) * kOutBytes;
           // 16-byte chunk c of row r at c ^ ((r >> 1) & 3): the box' 64-byte swizzle
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -417,15 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
               for (int j = 0; j < 4; ++j) ptx::unpack_f32x2(acc[i][4 * c + j], f[2 * j], f[2 * j + 1]);
               v = bf16_pack(f);
             }
-            *reinterpret_cast<uint4*>(outb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v;
+            *reinterpret_cast<uint4*>(outb + ob + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v;
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (p.accumulate)
-              ptx::tma_add_box3(&maps.dw, out_s, k0, n0, x.g);
+              ptx::tma_add_box3(&maps.dw, out_s + ob, k0, n0, x.g);
             else
-              ptx::tma_store_box3(&maps.dw, out_s, k0, n0, x.g);
+              ptx::tma_store_box3(&maps.dw, out_s + ob, k0, n0, x.g);
             ptx::bulk_commit();
           }
         }
