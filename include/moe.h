@@ -1,6 +1,7 @@
 /*
  * moe.h -- C ABI of libmoe_gb300.so: the single-GPU forward of one
- * Mixture-of-Experts FFN layer on GB300 (sm_103a).
+ * Mixture-of-Experts FFN layer on GB300 (sm_103a), and the operators that
+ * train its routed experts in 8 bits (at the end).
  *
  * The layer, as the page "MOE推理流程解析" (ffner.com) lays it out:
  *   section 三: the router scores every eligible expert; top-k keeps the

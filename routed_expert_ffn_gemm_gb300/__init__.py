@@ -1,4 +1,5 @@
-"""GB300-native forward of one Mixture-of-Experts FFN layer.
+"""GB300-native forward of one Mixture-of-Experts FFN layer, and the operators
+that train its routed experts in 8 bits.
 
 The compute path is a C-ABI CUDA library (``libmoe_gb300.so``, kernels for
 sm_103a) reached through the thin ctypes binding in ``api``.  Importing this
