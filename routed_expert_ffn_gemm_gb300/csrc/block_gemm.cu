@@ -31,24 +31,20 @@
 //
 // Transposed weights ([E, K, N]: the data gradient with the forward's
 // arrays) are the same tiles read MN-major by the MMA.
-#include <atomic>
-
-#include "ptx.cuh"
-#include "train.cuh"
+#include "block_gemm.cuh"
 
 namespace moe {
 namespace {
+
+using namespace block_gemm;
 
 constexpr int kThreads = 384;
 constexpr int kOwnBytes = 128 * 128;          // the CTA's own operand (M side): 128 rows of 128 codes
 constexpr int kGroup = 4, kScaleRing = 2;     // blocks of a step; steps' scales in flight
 constexpr int kEpiWarps = 8;
-constexpr int kBand = 16;                     // row tiles that share a pass over the weights
 constexpr int kChunks = 4;                    // chunks of 32 columns of an accumulating warp
 constexpr int kOutPitch = 36;                 // words of a staged pair of rows (32 channels), padded against conflicts
-constexpr int kOutBytes = 2048;               // staging of an accumulating warp: 32 rows of 64 bytes
 static_assert(8 * 4 * kOutPitch <= kOutBytes, "staged pairs of rows");
-constexpr int kMaxGroups = 1024;
 
 // Tiles of up to 256 rows, or (FEW) 64: with few rows an expert, weights are
 // all that moves, and slots of 24 KB instead of 48 keep twice as many of them
@@ -85,23 +81,6 @@ constexpr int kRowsOnM = 129;
 constexpr int kRegsLow = 72, kRegsHigh = 216;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split");
 
-struct Params {
-  int R, K, N, E, MT, KB, NB;
-  int out_f32;
-  const float* a_scales;
-  const float* w_scales;
-  const int32_t* offsets;
-  void* out;
-  int* status;
-  long long timeout_ns;
-};
-
-struct Maps {
-  CUtensorMap w;
-  CUtensorMap a[4];  // boxes of 16, 32, 64, 128 rows
-  CUtensorMap out;   // 32 rows of 64 bytes
-};
-
 struct Unit {
   int g, row0, n_valid, n_mma, mt, tiles;
   int batch;  // blocks whose sums share an accumulator buffer, 256 / batch columns each
@@ -110,33 +89,17 @@ struct Unit {
 
 template <bool FEW>
 __device__ __forceinline__ Unit unit_of(int u, const int* offs, const int* prefix, int E, int MT) {
-  constexpr int ROWS = Tile<FEW>::ROWS;
-  const int t = u / MT;
-  int lo = 0, hi = E - 1;  // the expert whose tiles hold t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
-  }
+  const Place t = place_of<Tile<FEW>::ROWS>(u, offs, prefix, E, MT);
   Unit x;
-  x.g = lo;
-  x.tiles = prefix[lo + 1] - prefix[lo];
-  const int l = u - prefix[lo] * MT;
-  const int band = l / (kBand * MT), rem = l - band * (kBand * MT);
-  const int wide = min(kBand, x.tiles - band * kBand);
-  x.mt = rem / wide;
-  const int rt = band * kBand + rem % wide;
-  const int r0 = rt * ROWS;
-  x.row0 = offs[lo] + r0;
-  x.n_valid = min(ROWS, offs[lo + 1] - x.row0);
+  x.g = t.g;
+  x.tiles = t.tiles;
+  x.mt = t.mt;
+  x.row0 = t.row0;
+  x.n_valid = t.n_valid;
   x.rows_m = !FEW && x.n_valid >= kRowsOnM;
-  x.n_mma = x.rows_m ? ROWS : (x.n_valid + 31) / 32 * 32;  // (two boxes of at least 16)
+  x.n_mma = x.rows_m ? Tile<FEW>::ROWS : (x.n_valid + 31) / 32 * 32;  // (two boxes of at least 16)
   x.batch = x.rows_m ? 1 : FEW || x.n_mma <= 64 ? 4 : 2;
   return x;
-}
-
-// All lanes of the warp wait; the warp agrees on the outcome.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t deadline, volatile int* abort) {
-  return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, deadline, abort)) != 0;
 }
 
 // Adds one accumulator buffer to a warp's registers, acc += scale * D.  The
@@ -248,64 +211,6 @@ __device__ __forceinline__ void store_rows_n(const Params& p, const Unit& x, con
   }
 }
 
-// Rows on M: the lane's row is r0 + lane of the unit, acc[i][j] channel
-// ch0 + 64 i + j.  64 bytes of each row at a time: by a TMA store when all 32
-// rows are the unit's (it clips the channels past N), else row by row.
-// 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3), as the store's 64-byte
-// swizzle has it.
-__device__ __forceinline__ void store_rows_m(const Params& p, const CUtensorMap* map, const Unit& x,
-                                             const float (&acc)[kChunks][32], int r0, int ch0, uint8_t* outb) {
-  const int lane = threadIdx.x & 31;
-  if (r0 >= x.n_valid) return;
-  const bool whole = r0 + 32 <= x.n_valid;
-  const int es = p.out_f32 ? 4 : 2, per = 64 / es;  // channels in 64 bytes
-  uint8_t* out = static_cast<uint8_t*>(p.out) + (size_t)(x.row0 + r0) * p.N * es;
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k == 1 && !p.out_f32) break;
-      const int ch = ch0 + 64 * i + k * per;
-      if (ch >= p.N) break;
-      if (lane == 0) ptx::bulk_wait_read<0>();  // the previous store has read the staged rows
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint4 v;
-        if (p.out_f32) {
-          const float* f = &acc[i][16 * k + 4 * c];
-          v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-        } else {
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = acc[i][8 * c + j];
-          v = bf16_pack(f);
-        }
-        *reinterpret_cast<uint4*>(outb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v;
-      }
-      if (whole) {
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::tma_store_2d(map, ptx::smem_u32(outb), ch, x.row0 + r0);
-          ptx::bulk_commit();
-        }
-        continue;
-      }
-      __syncwarp();
-      const int c = lane & 3;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int r = 8 * h + (lane >> 2);
-        const uint4 t = *reinterpret_cast<const uint4*>(outb + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-        if (r0 + r < x.n_valid && ch + c * (16 / es) < p.N)
-          *reinterpret_cast<uint4*>(out + (size_t)r * p.N * es + (size_t)ch * es + c * 16) = t;
-      }
-      __syncwarp();
-    }
-  }
-}
-
 template <bool TRANS, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p, const __grid_constant__ Maps maps) {
   using T = Tile<FEW>;
@@ -361,33 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
   griddep_wait();
   griddep_launch_dependents();
 
-  // group ranges, clamped into [0, R], and the prefix of their tile counts
-  for (int g = threadIdx.x; g <= p.E; g += kThreads) {
-    int o = p.offsets[g];
-    if (o < 0 || o > p.R) {
-      set_device_status(p.status, MOE_ERR_DEVICE_BOUNDS);
-      o = o < 0 ? 0 : p.R;
-    }
-    offs[g] = o;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    ordered_offsets(offs, p.E, p.status);
-    int run = 0;
-    for (int g0 = 0; g0 < p.E; g0 += 32) {
-      const int g = g0 + lane;
-      const int n = g < p.E ? (offs[g + 1] - offs[g] + kBN - 1) / kBN : 0;
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (g < p.E) prefix[g] = run + incl - n;
-      run += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) prefix[p.E] = run;
-  }
+  row_tiles<kBN>(p, offs, prefix, kThreads);
   ptx::tc_fence_before();
   ptx::cluster_sync();  // (also: the peer's barriers are initialised)
   ptx::tc_fence_after();
@@ -634,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
       // (worked out again: the registers hold sums during the loop)
       const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
       if (!FEW && x.rows_m)
-        store_rows_m(p, &maps.out, x, acc, (int)rank * 128 + q * 32, x.mt * 256 + eg * 32, outb);
+        store_rows_m<kChunks, 64>(p, &maps.out, x.row0, x.n_valid, acc, (int)rank * 128 + q * 32, x.mt * 256 + eg * 32, outb);
       else
         store_rows_n(p, x, acc, x.mt * 256 + (int)rank * 128 + q * 32, eg * 32, outb);
     }
@@ -651,48 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
   }
 }
 
-// CTAs (two per pair) that are resident at once: the grid is persistent and
-// not every SM finds a partner.  One value per device, written once.
-template <bool TRANS, bool FEW>
-moe_status resident_ctas(int* out) {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  MOE_TRY_CUDA(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
-  int n = known[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    auto kern = block_gemm_kernel<TRANS, FEW>;
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<FEW>::SMEM_BYTES));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Tile<FEW>::SMEM_BYTES;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    MOE_TRY_CUDA(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
-    if (n < 1) return MOE_ERR_UNSUPPORTED;
-    known[dev].store(n, std::memory_order_relaxed);
-  }
-  *out = 2 * n;
-  return MOE_OK;
-}
-
 template <bool TRANS, bool FEW>
 moe_status launch(const Params& p, const Maps& maps, int num_sms, cudaStream_t s) {
-  int ctas = 0;
-  MOE_TRY((resident_ctas<TRANS, FEW>(&ctas)));
+  static std::atomic<int> known[64];
   // no more pairs than units can exist: whole row tiles, and one per group
   const long long tiles = (long long)p.R / Tile<FEW>::ROWS + (p.R < p.E ? p.R : p.E);
-  const long long units = tiles * p.MT;
-  int grid = ctas < num_sms ? ctas : num_sms & ~1;
-  if (2 * units < grid) grid = (int)(2 * units);
-  MOE_TRY_CUDA(launch_kc(2, block_gemm_kernel<TRANS, FEW>, dim3(grid), dim3(kThreads), Tile<FEW>::SMEM_BYTES, s, p, maps));
-  return MOE_OK;
+  return launch_clusters<2>(block_gemm_kernel<TRANS, FEW>, known, Tile<FEW>::SMEM_BYTES, tiles * p.MT, num_sms, s, p, maps);
 }
 
 }  // namespace
@@ -719,6 +562,10 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
     MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.K, a.N, a.N, 1, 128, 128, 128));
   else
     MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.N, a.K, a.K, 1, 128, 128, 128));
+  if (a.transposed)
+    MOE_TRY(make_tmap_3d(&maps.w64, a.w, a.E, a.K, a.N, a.N, 1, 128, 64, 64));
+  else
+    MOE_TRY(make_tmap_3d(&maps.w64, a.w, a.E, a.N, a.K, a.K, 1, 64, 128, 128));
   for (int i = 0; i < 4; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K, 1, 16u << i, 128, 128));
   const int es = a.out_f32 ? 4 : 2;
   MOE_TRY(make_tmap_2d(&maps.out, a.out, a.R, a.N, es, 32, 64 / es, 64));
@@ -726,6 +573,8 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
   // several tiles, whose weights come from L2 again).  64 experts of 7168 x
   // 4096 with 40 rows each: 303 us in tiles of 64, 349 in tiles of 256.
   const bool few = a.R <= 64 || (long long)a.R <= 48ll * a.E;
+  // Several whole tiles an expert on average: clusters of four.
+  if ((long long)a.R >= kManyRows * a.E) return block_gemm_many_launch(p, maps, a.transposed, a.num_sms, s);
   if (few) return a.transposed ? launch<true, true>(p, maps, a.num_sms, s) : launch<false, true>(p, maps, a.num_sms, s);
   return a.transposed ? launch<true, false>(p, maps, a.num_sms, s) : launch<false, false>(p, maps, a.num_sms, s);
 }

@@ -66,6 +66,21 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Two at once (bit i: barrier i's phase has completed): the polls overlap.
+__device__ __forceinline__ uint32_t mbar_test2(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+  uint32_t a, b;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%2], %3;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%4], %5;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "selp.u32 %1, 2, 0, q;\n\t}\n"
+      : "=r"(a), "=r"(b)
+      : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
+      : "memory");
+  return a | b;
+}
+
 // ---------------------------------------------------------------------------
 // clusters (CTA pairs)
 // ---------------------------------------------------------------------------
@@ -219,6 +234,15 @@ __device__ __forceinline__ void tma_load_box3(uint32_t dst, const CUtensorMap* m
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+// The same, completing a barrier that may sit in either CTA of the pair.
+__device__ __forceinline__ void tma_load_box3_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster,
+                                                   int32_t c0, int32_t c1, int32_t c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
 // The same into the shared memory of every CTA of the cluster whose bit is set
@@ -387,6 +411,17 @@ __device__ __forceinline__ void mma_f8_one(uint32_t one, uint32_t d_tmem, uint64
       "setp.ne.b32 q, %4, 0;\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(one), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_f8_pair_one(uint32_t one, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(one), "n"(ACC ? 1 : 0)
       : "memory");
 }
@@ -605,6 +640,17 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr, uint32_t 
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
+  return d;
+}
+// The same with rows of 64 bytes under 64-byte swizzling, 8-row groups 512
+// bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn_sw64(uint32_t smem_addr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(mn_stride >> 4) << 16;
+  d |= (uint64_t)(512 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;  // swizzle 64B
   return d;
 }
 // Instruction descriptor bits of MN-major operands.
