@@ -20,7 +20,8 @@
 // the CTA; with one MMA for both CTAs that round trip crosses them and bounds
 // the loop.
 // Units run row tiles first inside bands of 16, so that a weight tile is read
-// from memory once while the band's rows stay in L2.
+// from memory once while the band's rows stay in L2.  (From kManyRows rows an
+// expert on average the product is block_gemm_many.cu's.)
 //
 // Roles: warp 0 copies (TMA), warp 1 issues the MMAs, warp 2 brings the
 // scales to shared memory (cp.async), warps 4..11 hold the accumulators:
@@ -76,6 +77,7 @@ struct Tile {
 // experts of 7168 x 4096 with 120 rows each took 404 us on N and 438 on M;
 // 80 rows 375 and 434.
 constexpr int kRowsOnM = 129;
+static_assert(kRowsOnM <= 129, "a batch of two blocks has 128 columns each");
 // Registers: 384 x 168 at launch; the accumulating warps take what the
 // other warpgroup gives back.
 constexpr int kRegsLow = 72, kRegsHigh = 216;
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
       // (worked out again: the registers hold sums during the loop)
       const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
       if (!FEW && x.rows_m)
-        store_rows_m<kChunks, 64>(p, &maps.out, x.row0, x.n_valid, acc, (int)rank * 128 + q * 32, x.mt * 256 + eg * 32, outb);
+        store_rows_m<1, kChunks, 64>(p, &maps.out, x.row0, x.n_valid, acc, (int)rank * 128 + q * 32, x.mt * 256 + eg * 32, outb);
       else
         store_rows_n(p, x, acc, x.mt * 256 + (int)rank * 128 + q * 32, eg * 32, outb);
     }
@@ -557,24 +559,21 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;
   if (((long long)a.R / Tile<true>::ROWS + a.E) * p.MT > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  const bool many = (long long)a.R >= kManyRows * a.E;
+  const int channels = many ? 64 : 128;  // of a weight box
   Maps maps;
   if (a.transposed)
-    MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.K, a.N, a.N, 1, 128, 128, 128));
+    MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.K, a.N, a.N, 1, 128, channels, channels));
   else
-    MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.N, a.K, a.K, 1, 128, 128, 128));
-  if (a.transposed)
-    MOE_TRY(make_tmap_3d(&maps.w64, a.w, a.E, a.K, a.N, a.N, 1, 128, 64, 64));
-  else
-    MOE_TRY(make_tmap_3d(&maps.w64, a.w, a.E, a.N, a.K, a.K, 1, 64, 128, 128));
-  for (int i = 0; i < 4; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K, 1, 16u << i, 128, 128));
+    MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.N, a.K, a.K, 1, channels, 128, 128));
+  for (int i = many ? 3 : 0; i < 4; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K, 1, 16u << i, 128, 128));
   const int es = a.out_f32 ? 4 : 2;
   MOE_TRY(make_tmap_2d(&maps.out, a.out, a.R, a.N, es, 32, 64 / es, 64));
+  if (many) return block_gemm_many_launch(p, maps, a.transposed, a.num_sms, s);
   // Few rows an expert on average (a group of more than 64 rows then takes
   // several tiles, whose weights come from L2 again).  64 experts of 7168 x
   // 4096 with 40 rows each: 303 us in tiles of 64, 349 in tiles of 256.
   const bool few = a.R <= 64 || (long long)a.R <= 48ll * a.E;
-  // Several whole tiles an expert on average: clusters of four.
-  if ((long long)a.R >= kManyRows * a.E) return block_gemm_many_launch(p, maps, a.transposed, a.num_sms, s);
   if (few) return a.transposed ? launch<true, true>(p, maps, a.num_sms, s) : launch<false, true>(p, maps, a.num_sms, s);
   return a.transposed ? launch<true, false>(p, maps, a.num_sms, s) : launch<false, false>(p, maps, a.num_sms, s);
 }

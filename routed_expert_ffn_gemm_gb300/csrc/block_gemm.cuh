@@ -25,8 +25,7 @@ struct Params {
 };
 
 struct Maps {
-  CUtensorMap w;     // 128 x 128
-  CUtensorMap w64;   // 64 (channels, or the reduction when transposed) x 128
+  CUtensorMap w;     // 128 of the reduction x 128 channels (block_gemm_many.cu: 64)
   CUtensorMap a[4];  // boxes of 16, 32, 64, 128 rows
   CUtensorMap out;   // 32 rows of 64 bytes
 };
@@ -96,16 +95,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
   return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, deadline, abort)) != 0;
 }
 
-// One warp's accumulators to memory, rows on M: the lane's row is r0 + lane of the unit, acc[i][j] channel
-// ch0 + STRIDE i + j.  64 bytes of each row at a time: by a TMA store when all 32
-// rows are the unit's (it clips the channels past N), else row by row.
+// One warp's accumulators to memory, rows on M: the lane's row is r0 + lane of
+// the unit, acc[i][j] channel ch0 + STRIDE i + j.  64 bytes of each row at a
+// time, staged in BUFS buffers in turn: by a TMA store when all 32 rows are
+// the unit's (it clips the channels past N), else row by row.
 // 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3), as the store's 64-byte
 // swizzle has it.
-template <int CHUNKS, int STRIDE>
+template <int BUFS, int CHUNKS, int STRIDE>
 __device__ __forceinline__ void store_rows_m(const Params& p, const CUtensorMap* map, int row0, int n_valid,
-                                             const float (&acc)[CHUNKS][32], int r0, int ch0, uint8_t* outb) {
+                                             const float (&acc)[CHUNKS][32], int r0, int ch0, uint8_t* out0) {
   const int lane = threadIdx.x & 31;
   if (r0 >= n_valid) return;
+  if (BUFS > 1 && lane == 0) ptx::bulk_wait_read<0>();  // (the unit before may have ended on either buffer)
   const bool whole = r0 + 32 <= n_valid;
   const int es = p.out_f32 ? 4 : 2, per = 64 / es;  // channels in 64 bytes
   uint8_t* out = static_cast<uint8_t*>(p.out) + (size_t)(row0 + r0) * p.N * es;
@@ -116,7 +117,8 @@ __device__ __forceinline__ void store_rows_m(const Params& p, const CUtensorMap*
       if (k == 1 && !p.out_f32) break;
       const int ch = ch0 + STRIDE * i + k * per;
       if (ch >= p.N) break;
-      if (lane == 0) ptx::bulk_wait_read<0>();  // the previous store has read the staged rows
+      uint8_t* outb = out0 + (BUFS == 1 ? 0 : (p.out_f32 ? k : i) % BUFS) * kOutBytes;
+      if (lane == 0) ptx::bulk_wait_read<BUFS - 1>();  // the store before has read this buffer
       __syncwarp();
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -191,9 +193,12 @@ moe_status launch_clusters(Kernel kern, std::atomic<int> (&known)[64], int smem,
 
 }  // namespace block_gemm
 
-// From this many rows an expert on average the product runs on clusters of
-// four (block_gemm_many.cu).
-constexpr long long kManyRows = 256;
+// From this many rows an expert on average the product runs on
+// block_gemm_many.cu.  64 experts of 7168 x 4096, us there and in
+// block_gemm.cu: 80 rows 396 and 375, 100 rows 397 and 404, 120 rows 391 and
+// 403, 160 rows 393 and 429; 90 rows unevenly spread 417 and 389; one expert
+// with 100 rows 31 and 34.
+constexpr long long kManyRows = 100;
 moe_status block_gemm_many_launch(const block_gemm::Params& p, const block_gemm::Maps& maps, bool transposed,
                                   int num_sms, cudaStream_t s);
 

@@ -1,7 +1,27 @@
-// The block product (block_gemm.cu) where experts have many rows: 256 rows x
-// 256 channels of one expert a unit on a pair of CTAs with one MMA for both
-// (cta_group::2), 128 rows and half of the channels' weights a CTA.
+// The block product (block_gemm.cu) where experts have many rows: a unit is 256
+// rows x 256 channels of one expert on a pair of CTAs with one MMA for both
+// (cta_group::2, M = 256): each CTA holds 128 rows and the weights of half of
+// the channels, 32 KB a block of 128, where MMAs of its own would need 48.
+// (Shared memory bounds those: 48 KB written and 48 KB read a block at 128
+// bytes a cycle are 768 cycles, the block's MMAs 512.)
 //
+// Rows are the MMA's M side, so a lane of tensor memory is a row and its scale
+// one value a block and 128 channels.  The two halves of 128 channels have two
+// buffers of 128 columns each, are issued by a warp each (1 and 3 of the even
+// CTA) and added by four warps of each CTA each (4..11), so that one half is
+// on its way while the other is read.  Warp 0 of each CTA copies, warp 2
+// brings the scales.
+//
+// What bounds it is the adding warps' chain of waits: a block of 8192 rows x
+// 4096 x 14336 takes a pair about 1000 cycles, its MMAs 512, its copies some
+// 650, its adds 256 issue slots; two warps a scheduler (128 sums a lane, all
+// of the register file) do not hide the waits for a barrier, for tensor memory
+// and for shared memory, which MMAs and copies keep busy.  Hence the reads
+// ahead: a group's scales at once (460 -> 427 us), the next buffer's barrier
+// polled while this one is added (427 -> 415), two staged store boxes (415 ->
+// 402).  Measured: 8192 rows of 4 experts 4096 -> 14336 in 399 us, 2.4 PFLOP/s;
+// clusters of four with an MMA for each CTA and four buffers took 606, a
+// quarter of the columns a hand-over 590, one issuing warp for both halves 483.
 #include "block_gemm.cuh"
 
 namespace moe {
@@ -12,15 +32,16 @@ using namespace block_gemm;
 constexpr int kThreads = 384;
 constexpr int kTileBytes = 128 * 128;         // an operand: 128 rows or channels, 128 codes of the reduction
 constexpr int kHalfBytes = kTileBytes / 2;    // 64 channels of each half of 128
-constexpr int kStages = 6, kStageBytes = 2 * kTileBytes;
-constexpr int kBuffers = 4;                   // of 128 columns
-constexpr int kGroup = 4, kScaleRing = 4;     // blocks whose scales are handed over at once; such groups in flight
+constexpr int kStages = 5, kStageBytes = 2 * kTileBytes;
+constexpr int kBuffers = 4;                   // of 128 columns: two for each half
+constexpr int kGroup = 4, kScaleRing = 3;     // blocks whose scales are handed over at once; such groups in flight
 constexpr int kEpiWarps = 8, kChunks = 4;     // chunks of 32 channels of an accumulating warp
+constexpr int kOutBufs = 2;                   // staged store boxes of an accumulating warp
 constexpr int kOutOff = kStages * kStageBytes;
-constexpr int kScaleOff = kOutOff + kEpiWarps * kOutBytes;
+constexpr int kScaleOff = kOutOff + kEpiWarps * kOutBufs * kOutBytes;
 constexpr int kWScaleOff = kScaleOff + kScaleRing * kGroup * 128 * 4;
 constexpr int kBarOff = kWScaleOff + kScaleRing * kGroup * 8;  // [ring][half][block]
-// full[S], empty[S], acc_full[4], acc_empty[4], scale_full[4], scale_empty[4], drain[2]
+// full[S], empty[S], acc_full[4], acc_empty[4], scale_full[3], scale_empty[3], drain[2]
 constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 2 * kScaleRing + 2;
 constexpr int kSlotOff = kBarOff + 8 * kNumBars;
 constexpr int kAbortOff = kSlotOff + 8;
@@ -83,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
     ptx::fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    ptx::prefetch_tmap(&maps.w64);
+    ptx::prefetch_tmap(&maps.w);
     ptx::prefetch_tmap(&maps.a[3]);
     ptx::prefetch_tmap(&maps.out);
   }
@@ -122,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
           ptx::tma_load_2d_pair(at, &maps.a[3], fb, kb * 128, row, keep);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            ptx::tma_load_box3_pair(at + kTileBytes + h * kHalfBytes, &maps.w64, fb, TRANS ? ch + 128 * h : kb * 128,
+            ptx::tma_load_box3_pair(at + kTileBytes + h * kHalfBytes, &maps.w, fb, TRANS ? ch + 128 * h : kb * 128,
                                     TRANS ? kb * 128 : ch + 128 * h, x.g, keep);
         }
       }
@@ -220,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
     // ------------------------------------------------------- accumulation
     ptx::regs_inc<kRegsHigh>();
     const int q = warp & 3, h = (warp - 4) >> 2, row = q * 32 + lane;
-    uint8_t* outb = smem + kOutOff + (warp - 4) * kOutBytes;
+    uint8_t* outb = smem + kOutOff + (warp - 4) * kOutBufs * kOutBytes;
     const uint32_t at = tmem_base + ((uint32_t)(q * 32) << 16) + h * 128;
     const uint32_t lead_acce = lead(acce_bar((uint32_t)h));
     uint32_t it = 0, sit = 0;
@@ -236,15 +257,16 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
         ok = warp_wait(sfull_bar(ring), (sit / kScaleRing) & 1u, deadline, abort_flag);
         if (!ok) break;
         // the group's scales at once: a shared-memory read in front of each
-        // block takes some 300 cycles while MMAs and copies use the memory
+        // block waits behind the memory's other users
         const float4 sa = *reinterpret_cast<const float4*>(scales + (ring * 128 + row) * kGroup);
         const float4 sw = *reinterpret_cast<const float4*>(wscales + (ring * 2 + h) * kGroup);
         float f = sa.x * sw.x, f1 = sa.y * sw.y, f2 = sa.z * sw.z, f3 = sa.w * sw.w;
         const int n = min(kGroup, p.KB - kb0);
+        bool seen = ptx::mbar_test_wait(accf_bar(2 * (it & 1u) + h), (it >> 1) & 1u);
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++it) {
           const uint32_t buf = it & 1u;
-          ok = warp_wait(accf_bar(2 * buf + h), (it >> 1) & 1u, deadline, abort_flag);
+          ok = __all_sync(0xffffffffu, seen) || warp_wait(accf_bar(2 * buf + h), (it >> 1) & 1u, deadline, abort_flag);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t from = at + 256u * buf;
@@ -259,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
               ptx::tc_fence_before();
               __syncwarp();
               if (lane == 0) ptx::mbar_arrive_cluster(lead_acce + 16u * buf);
+              seen = ptx::mbar_test_wait(accf_bar(2 * (buf ^ 1u) + h), ((it + 1) >> 1) & 1u);
             }
 #pragma unroll
             for (int k = 0; k < 32; ++k) acc[t][k] = fmaf(__uint_as_float(d[t & 1][k]), f, acc[t][k]);
@@ -273,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
       }
       if (!ok) break;
       const Place x = place_of<256>(u, offs, prefix, p.E, p.MT);
-      store_rows_m<kChunks, 32>(p, &maps.out, x.row0, x.n_valid, acc, (int)rank * 128 + q * 32, x.mt * 256 + h * 128,
+      store_rows_m<kOutBufs, kChunks, 32>(p, &maps.out, x.row0, x.n_valid, acc, (int)rank * 128 + q * 32, x.mt * 256 + h * 128,
                                 outb);
     }
     if (lane == 0) ptx::bulk_wait_all();

@@ -547,3 +547,46 @@ def test_block_gemm_tiles_of_every_size_in_turn(K, transposed):
         assert torch.equal(api.grouped_block_gemm(*args, transposed, out_dtype=torch.float32), got)
     y, mag = ref.block_gemm(a, sa, off, w, sw, transposed)
     assert ((got.cpu().double() - y).abs() <= (32 + 4 * ref.blocks(K)) * U * mag).all()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("transposed", [False, True], ids=["forward", "gradient"])
+@pytest.mark.parametrize("K,N", [(16, 16), (144, 1296), (640, 400), (1152, 272)])
+def test_block_gemm_many_rows_an_expert(K, N, transposed, out_dtype):
+    # several tiles an expert on average, groups and matrices that end
+    # anywhere in one, and more units than CTA pairs
+    counts = [700, 0, 257, 1, 900, 385, 31, 5200, 33]
+    R, a, sa, off, w, sw = gemm_case(counts, 3, 2, K, N, transposed, seed=K)
+    assert R >= 256 * len(counts)
+    args = [t.to(DEV) for t in (a, sa, off, w, sw)]
+    out = Guarded((R, N), out_dtype, DEV)
+    out.t.fill_(-77.0)
+    api.grouped_block_gemm(*args, transposed, out=out.t)
+    got = out.t.clone()
+    for _ in range(10):
+        api.grouped_block_gemm(*args, transposed, out=out.t)
+        assert torch.equal(out.t, got)
+    got = got.cpu().double()
+    y, mag = ref.block_gemm(a, sa, off, w, sw, transposed)
+    inside = torch.zeros(R, dtype=torch.bool)
+    inside[3:3 + sum(counts)] = True
+    assert (got[~inside] == -77.0).all(), "rows of no expert were written"
+    tol = (32 + 4 * ref.blocks(K)) * U * mag + (2.0 ** -8 * y.abs() if out_dtype == torch.bfloat16 else 0)
+    assert ((got - y).abs()[inside] <= tol[inside]).all(), float(((got - y).abs() / tol)[inside].max())
+    assert out.intact()
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["forward", "gradient"])
+def test_block_gemm_many_rows_keep_experts_apart(transposed):
+    counts, K, N = [400, 333, 290], 144, 176
+    R, a, sa, off, w, sw = gemm_case(counts, 0, 0, K, N, transposed, seed=3)
+    clean = api.grouped_block_gemm(a.to(DEV), sa.to(DEV), off.to(DEV), w.to(DEV), sw.to(DEV), transposed)
+    a2, sa2, w2 = a.clone(), sa.clone(), w.clone()
+    a2[400:733] = 0x7F
+    sa2[400:733] = float("inf")
+    w2[1] = 0x7F
+    got = api.grouped_block_gemm(a2.to(DEV), sa2.to(DEV), off.to(DEV), w2.to(DEV), sw.to(DEV), transposed)
+    keep = torch.ones(R, dtype=torch.bool)
+    keep[400:733] = False
+    assert torch.equal(got.cpu()[keep], clean.cpu()[keep])
+    assert torch.isnan(got[400:733]).all()
