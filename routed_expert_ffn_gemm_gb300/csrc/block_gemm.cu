@@ -17,8 +17,8 @@
 // loads half of what both share and multicasts it, so that L2 gives every
 // byte once a cluster.  The MMAs are each CTA's own (cta_group::1): a block's
 // sum goes from the tensor cores to the registers and the buffer back within
-// the CTA; with one MMA for both CTAs that round trip crosses them and bounds
-// the loop.
+// the CTA; with one MMA of 256 columns for both CTAs that round trip crosses
+// them and bounds the loop.
 // Units run row tiles first inside bands of 16, so that a weight tile is read
 // from memory once while the band's rows stay in L2.  (From kManyRows rows an
 // expert on average the product is block_gemm_many.cu's.)
