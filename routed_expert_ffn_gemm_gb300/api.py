@@ -465,11 +465,13 @@ def _exact(t: Optional[torch.Tensor], name: str, shape, dtype) -> None:
 
 def _rows(t: torch.Tensor, name: str, dtype=None) -> int:
     """The row pitch in elements of a matrix whose rows may lie apart."""
-    if t.dim() != 2 or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name}: {t.dtype} {list(t.shape)}, the call takes a matrix" + (f" of {dtype}" if dtype else ""))
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    shape = t.shape
+    if len(shape) != 2 or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{name}: {t.dtype} {list(shape)}, the call takes a matrix" + (f" of {dtype}" if dtype else ""))
+    (rows, cols), (pitch, step) = shape, t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and pitch < cols):
         raise ValueError(f"{name}: the elements of a row must be adjacent and rows must not overlap")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return pitch if rows > 1 else cols
 
 
 def _pitched(t: torch.Tensor) -> int:
@@ -483,13 +485,18 @@ def quantize_blocks(x, scale="amax", codes=None, scales=None, stream=None):
     may lie apart): (codes uint8 [..., cols], scales fp32 [..., blocks])."""
     if scale not in SCALE:
         raise ValueError(f"scale: {scale!r}, the call takes {sorted(SCALE)}")
-    kind, cols = _type(x.dtype, "x"), int(x.shape[-1])
-    m = x if x.dim() == 2 else x.reshape(-1, cols)
-    ld, sshape = _rows(m, "x"), (*x.shape[:-1], _blocks(cols))
-    codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device) if codes is None else codes
-    scales = torch.empty(sshape, dtype=torch.float32, device=x.device) if scales is None else scales
-    _exact(codes, "codes", x.shape, torch.uint8)
-    _exact(scales, "scales", sshape, torch.float32)
+    kind, shape, dev = _type(x.dtype, "x"), x.shape, x.device
+    cols = shape[-1]
+    m = x if len(shape) == 2 else x.reshape(-1, cols)
+    ld, sshape = _rows(m, "x"), (*shape[:-1], _blocks(cols))
+    if codes is None:
+        codes = torch.empty(shape, dtype=torch.uint8, device=dev)
+    else:
+        _exact(codes, "codes", shape, torch.uint8)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+    else:
+        _exact(scales, "scales", sshape, torch.float32)
     _call("moe_quantize_blocks_e4m3", m.shape[0], cols, kind, SCALE[scale], _pitched(m), ld, _ptr(codes), _ptr(scales),
           _stream(stream))
     return codes, scales
@@ -544,15 +551,12 @@ def swiglu_save(g, u, want_h=False, want_codes=True, stream=None) -> SwigluSaved
     ld = _rows(g, "g", torch.bfloat16)
     if _rows(u, "u", torch.bfloat16) != ld or u.shape != g.shape:
         raise ValueError("g and u: two matrices of one shape and row pitch are expected")
-    R, f = g.shape
-
-    def new(*shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=g.device)
-
-    h = new(R, f, dtype=torch.bfloat16) if want_h else None
-    codes = new(R, f, dtype=torch.uint8) if want_codes else None
-    scales = new(R, _blocks(f), dtype=torch.float32) if want_codes else None
-    saved, saved_scales = new(2, R, f, dtype=torch.uint8), new(2, R, _blocks(f), dtype=torch.float32)
+    (R, f), dev, nb = g.shape, g.device, _blocks(g.shape[1])
+    h = torch.empty((R, f), dtype=torch.bfloat16, device=dev) if want_h else None
+    codes = torch.empty((R, f), dtype=torch.uint8, device=dev) if want_codes else None
+    scales = torch.empty((R, nb), dtype=torch.float32, device=dev) if want_codes else None
+    saved = torch.empty((2, R, f), dtype=torch.uint8, device=dev)
+    saved_scales = torch.empty((2, R, nb), dtype=torch.float32, device=dev)
     _call("moe_swiglu_save_e4m3", R, f, _pitched(g), _pitched(u), ld, _ptr(h), _ptr(codes), _ptr(scales), _ptr(saved),
           _ptr(saved_scales), _stream(stream))
     return SwigluSaved(h, codes, scales, saved, saved_scales)
