@@ -117,7 +117,7 @@ __device__ __forceinline__ void store_rows_m(const Params& p, const CUtensorMap*
       if (k == 1 && !p.out_f32) break;
       const int ch = ch0 + STRIDE * i + k * per;
       if (ch >= p.N) break;
-      uint8_t* outb = out0 + (BUFS == 1 ? 0 : (p.out_f32 ? k : i) % BUFS) * kOutBytes;
+      uint8_t* outb = out0 + ((p.out_f32 ? 2 * i + k : i) % BUFS) * kOutBytes;
       if (lane == 0) ptx::bulk_wait_read<BUFS - 1>();  // the store before has read this buffer
       __syncwarp();
 #pragma unroll

@@ -19,7 +19,9 @@
 // and for shared memory, which MMAs and copies keep busy.  Hence the reads
 // ahead: a group's scales at once (460 -> 427 us), the next buffer's barrier
 // polled while this one is added (427 -> 415), two staged store boxes (415 ->
-// 402).  Measured: 8192 rows of 4 experts 4096 -> 14336 in 399 us, 2.4 PFLOP/s;
+// 402), the unit's place handed on by warp 2 instead of searched for in front
+// of the stores (12 blocks a unit, 128 experts: 246 -> 234).  Measured: 8192
+// rows of 4 experts 4096 -> 14336 in 398 us, 2.4 PFLOP/s;
 // clusters of four with an MMA for each CTA and four buffers took 606, a
 // quarter of the columns a hand-over 590, one issuing warp for both halves 483.
 #include "block_gemm.cuh"
@@ -40,7 +42,8 @@ constexpr int kOutBufs = 2;                   // staged store boxes of an accumu
 constexpr int kOutOff = kStages * kStageBytes;
 constexpr int kScaleOff = kOutOff + kEpiWarps * kOutBufs * kOutBytes;
 constexpr int kWScaleOff = kScaleOff + kScaleRing * kGroup * 128 * 4;
-constexpr int kBarOff = kWScaleOff + kScaleRing * kGroup * 8;  // [ring][half][block]
+constexpr int kPlaceOff = kWScaleOff + kScaleRing * kGroup * 8;  // [ring][half][block]
+constexpr int kBarOff = kPlaceOff + kScaleRing * 16;             // row0, n_valid, mt of the group's unit
 // full[S], empty[S], acc_full[4], acc_empty[4], scale_full[3], scale_empty[3], drain[2]
 constexpr int kNumBars = 2 * kStages + 2 * kBuffers + 2 * kScaleRing + 2;
 constexpr int kSlotOff = kBarOff + 8 * kNumBars;
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
       ptx::mbar_init(acce_bar(b), kEpiWarps);  // (the even CTA's: a half's four warps of both CTAs)
     }
     for (int i = 0; i < kScaleRing; ++i) {
-      ptx::mbar_init(sfull_bar(i), 32);  // each lane's copies
+      ptx::mbar_init(sfull_bar(i), 33);  // each lane's copies, and the unit's place
       ptx::mbar_init(sempty_bar(i), kEpiWarps);
     }
     ptx::mbar_init(drain_bar(0), 1);
@@ -232,6 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
             ptx::cp_async4(sbase + kWScaleOff + ((ring * 2 + (lane & 1)) * kGroup + (lane >> 1)) * 4,
                            wp + (size_t)(kb + (lane >> 1)) * (TRANS ? p.NB : 1));
           ptx::cp_async_arrive_noinc(sfull_bar(ring));
+          if (lane == 0) {
+            *reinterpret_cast<int4*>(smem + kPlaceOff + ring * 16) = make_int4(x.row0, x.n_valid, x.mt, 0);
+            ptx::mbar_arrive(sfull_bar(ring));
+          }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -291,12 +298,16 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
           f2 = f3;
         }
         if (!ok) break;
+        if (kb0 + kGroup >= p.KB) break;  // (the last group's slot tells the unit's place first)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(sempty_bar(ring));
       }
       if (!ok) break;
-      const Place x = place_of<256>(u, offs, prefix, p.E, p.MT);
-      store_rows_m<kOutBufs, kChunks, 32>(p, &maps.out, x.row0, x.n_valid, acc, (int)rank * 128 + q * 32, x.mt * 256 + h * 128,
+      const uint32_t ring = sit++ % kScaleRing;
+      const int4 x = *reinterpret_cast<const int4*>(smem + kPlaceOff + ring * 16);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(sempty_bar(ring));
+      store_rows_m<kOutBufs, kChunks, 32>(p, &maps.out, x.x, x.y, acc, (int)rank * 128 + q * 32, x.z * 256 + h * 128,
                                 outb);
     }
     if (lane == 0) ptx::bulk_wait_all();
