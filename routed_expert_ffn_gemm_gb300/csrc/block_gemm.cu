@@ -320,6 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
           if (kb % kGroup == kGroup - 1 || kb == p.KB - 1) base = (base + kGroup) % kStages;
         }
       }
+      // every slot's last arrival, too, before the CTA may leave
+      for (int j = 0; j < kStages && ok; ++j)
+        ok = ptx::mbar_wait_bounded(empty_bar(j), ((used >> j) & 1u) ^ 1u, deadline, abort_flag);
       if (!ok) {
         set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
         // let issued copies land before shared memory is released (the peer's

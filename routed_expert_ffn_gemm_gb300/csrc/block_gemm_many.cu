@@ -150,6 +150,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
                                     TRANS ? kb * 128 : ch + 128 * h, x.g, keep);
         }
       }
+      // every slot's last arrival from the even CTA, too, before the CTA may leave
+      for (uint32_t j = it > kStages ? it - kStages : 0; j < it && ok; ++j)
+        ok = ptx::mbar_wait_bounded(empty_bar(j % kStages), (j / kStages) & 1u, deadline, abort_flag);
       if (!ok) {
         set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
         // let issued copies land before shared memory is released (the even

@@ -224,6 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const Params p, cons
           }
         }
       }
+      // every stage's last arrival from the even CTA, too, before the CTA may leave
+      for (long long j = issued > kStages ? issued - kStages : 0; j < issued && ok; ++j)
+        ok = ptx::mbar_wait_bounded(empty_bar((int)(j % kStages)), (uint32_t)((j / kStages) & 1), deadline, abort_flag);
       if (!ok) {
         set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
         const uint64_t grace = ptx::globaltimer_ns() + 100000000ull;

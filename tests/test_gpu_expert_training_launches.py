@@ -1,0 +1,44 @@
+"""The expert-training operators launched in other ways than one call at a
+time on the current stream: in quick succession, on given streams, from
+several threads, on results past 2^31 elements."""
+
+import pytest
+import torch
+
+from routed_expert_ffn_gemm_gb300 import api, build
+from tests import train_reference as ref
+from tests.test_gpu_expert_training import gemm_case, normal, offsets_of
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    build.build()
+    api._lib()
+    yield
+    assert api.moe_read_device_status() == api.OK
+
+
+def test_products_in_quick_succession():
+    # launches of one unit each, few rows, many rows and weight gradients in
+    # turn: each takes over shared memory and barriers that the one before
+    # has just left
+    cases = []
+    for counts, K, N, transposed in (([8], 128, 256, False), ([300], 128, 256, False), ([300], 272, 256, True),
+                                     ([40], 640, 128, True), ([90, 1], 256, 256, False)):
+        R, a, sa, off, w, sw = gemm_case(counts, 0, 0, K, N, transposed, seed=K)
+        args = [t.to(DEV) for t in (a, sa, off, w, sw)]
+        cases.append(lambda args=args, t=transposed: api.grouped_block_gemm(*args, t))
+    for rows, kind in ((5, "pow2"), (70, None)):
+        dy, x, xs, off = normal(rows, 256, seed=1).to(DEV), normal(rows, 256, seed=2), None, offsets_of([rows]).to(DEV)
+        if kind:
+            x, xs = ref.quantize(x, kind)
+            xs = xs.to(DEV)
+        x = x.to(DEV)
+        cases.append(lambda dy=dy, x=x, xs=xs, off=off: api.grouped_wgrad(dy, x, xs, off))
+    want = [c() for c in cases]
+    got = [[c() for c in cases] for _ in range(300)]
+    for row in got:
+        assert all(torch.equal(p, q) for p, q in zip(row, want))

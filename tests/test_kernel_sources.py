@@ -1,0 +1,28 @@
+"""Rules on the kernels' own sources that no launch can show."""
+
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "routed_expert_ffn_gemm_gb300", "csrc")
+SOURCES = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+def text_of(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+@pytest.mark.parametrize("name", ["block_gemm.cu", "block_gemm_many.cu", "wgrad.cu"])
+def test_copying_warp_waits_for_the_last_arrivals(name):
+    # The MMAs' commits arrive on a slot's barrier by themselves, at any time
+    # up to (and across the pair, after) the sums' own: the CTA whose barrier
+    # it is has to see the last one of each slot before it may leave.  So the
+    # copying warp waits for its slots once in the loop and once after it.
+    text = text_of(name)
+    role = text[text.index("- copies\n"):text.index("MOE_ERR_DEVICE_TIMEOUT", text.index("- copies\n"))]
+    loop, wait = role.index("for (int u = u_first"), r"mbar_wait_bounded\(\s*empty_bar\("
+    after = role[role.rindex("\n      }\n", loop):]  # behind the loop over the units
+    assert len(re.findall(wait, role)) == 2 and len(re.findall(wait, after)) == 1
