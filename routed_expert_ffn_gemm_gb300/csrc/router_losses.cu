@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(THREADS) router_losses_kernel(const RouterLoss
 // of sum_e c_e P_e through distributed shared memory.
 __global__ void __launch_bounds__(kSumThreads) __cluster_dims__(kSumCtas, 1, 1)
     router_losses_sum_kernel(const RouterLossArgs a, int nparts) {
+  ptx::cluster_arrive();  // (waited for in front of the first access to another CTA's memory)
   griddep_begin();
   constexpr int WARPS = kSumThreads / 32;
   __shared__ float sum_p[WARPS][32], red[WARPS];
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kSumThreads) __cluster_dims__(kSumCtas, 1, 1)
     zs = block_sum(zs, red);
     n = block_sum(n, red_n);
   }
+  ptx::cluster_wait();  // every CTA of the cluster has started
   if (threadIdx.x == 0) {
     const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&shares[rank]), 0u);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(dot) : "memory");

@@ -7,7 +7,7 @@ import torch
 
 from routed_expert_ffn_gemm_gb300 import api, build
 from tests import train_reference as ref
-from tests.test_gpu_expert_training import gemm_case, normal, offsets_of
+from tests.test_gpu_expert_training import close, gemm_case, normal, offsets_of, routed
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -42,3 +42,18 @@ def test_products_in_quick_succession():
     got = [[c() for c in cases] for _ in range(300)]
     for row in got:
         assert all(torch.equal(p, q) for p, q in zip(row, want))
+
+
+@pytest.mark.parametrize("E,k", [(2, 1), (8, 2), (40, 4), (256, 8), (1000, 8)])
+def test_router_sum_with_idle_ctas(E, k):
+    # with few experts most CTAs of the sum's cluster have nothing to add and
+    # hand their share over at once
+    T = 3000
+    logits, idx, _ = routed(T, E, k, seed=E)
+    want = ref.router(logits.double(), idx, None, 0.3, 0.02)
+    logits, idx = logits.to(DEV), idx.to(DEV)
+    runs = [api.router_losses(logits, idx, 0.3, 0.02) for _ in range(200)]
+    close(runs[0].loss, torch.stack(want[:2]))
+    assert torch.equal(runs[0].counts.cpu(), want[2])
+    for r in runs:
+        assert torch.equal(r.loss, runs[0].loss) and torch.equal(r.counts, runs[0].counts)

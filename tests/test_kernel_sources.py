@@ -26,3 +26,13 @@ def test_copying_warp_waits_for_the_last_arrivals(name):
     loop, wait = role.index("for (int u = u_first"), r"mbar_wait_bounded\(\s*empty_bar\("
     after = role[role.rindex("\n      }\n", loop):]  # behind the loop over the units
     assert len(re.findall(wait, role)) == 2 and len(re.findall(wait, after)) == 1
+
+
+def test_cluster_has_started_before_its_memory_is_written():
+    # distributed shared memory may be accessed once every CTA of the cluster
+    # runs: the sum over the router's parts needs a cluster barrier in front of
+    # its store to CTA 0
+    text = text_of("router_losses.cu")
+    kernel = text[text.index("    router_losses_sum_kernel("):]
+    before = kernel[: kernel.index("st.shared::cluster")]
+    assert "cluster_sync();" in before or before.index("cluster_arrive();") < before.index("cluster_wait();")
