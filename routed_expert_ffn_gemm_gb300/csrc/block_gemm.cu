@@ -14,11 +14,11 @@
 // scale is one value for all of a lane's columns.  With few rows they split
 // the channels (M side) and share the rows (N side, a multiple of 32), so
 // that few rows cost few columns; the scales then come per column.  Each CTA
-// loads half of what both share and multicasts it, so that L2 gives every
-// byte once a cluster.  The MMAs are each CTA's own (cta_group::1): a block's
-// sum goes from the tensor cores to the registers and the buffer back within
-// the CTA; with one MMA of 256 columns for both CTAs that round trip crosses
-// them and bounds the loop.
+// copies all that it needs by itself, so that nothing passes between them:
+// what both share comes from memory once and from L2 twice.  The MMAs are
+// each CTA's own (cta_group::1): a block's sum goes from the tensor cores to
+// the registers and the buffer back within the CTA; with one MMA of 256
+// columns for both CTAs that round trip crosses them and bounds the loop.
 // Units run row tiles first inside bands of 16, so that a weight tile is read
 // from memory once while the band's rows stay in L2.  (From kManyRows rows an
 // expert on average the product is block_gemm_many.cu's.)
@@ -31,7 +31,7 @@
 // (a hand-over costs some 500 cycles whatever it hands over).
 //
 // Bound by HBM with few rows an expert (512 rows on 230 of 256 experts of 2048
-// -> 7168: 468 us, 7.2 TB/s of weights; 8 rows on 8 experts of 7168 -> 4096:
+// -> 7168: 479 us, 7.1 TB/s of weights; 8 rows on 8 experts of 7168 -> 4096:
 // 43 us, 5.5 TB/s with launch and pipeline fill), by the hand-over of sums with
 // more.
 //
@@ -59,6 +59,7 @@ static_assert(8 * 4 * kOutPitch <= kOutBytes, "staged pairs of rows");
 template <bool FEW>
 struct Tile {
   static constexpr int ROWS = FEW ? 64 : 256;
+  static constexpr int BOX0 = FEW ? 0 : 2, BOXES = FEW ? 4 : 5;  // row boxes in use: Maps::a[BOX0] to [BOXES - 1]
   static constexpr int STEPS = FEW ? 2 : 1;               // steps in flight: block j of step i takes slot 4 (i % STEPS) + j
   static constexpr int STAGES = kGroup * STEPS;
   static constexpr int STAGE_BYTES = kOwnBytes + ROWS * 128;  // and the shared operand (N side)
@@ -79,8 +80,8 @@ struct Tile {
 };
 // From this many rows on a unit's rows are the MMA's M side (always 256 of
 // them), below it the N side (a multiple of 32): see the head of the file.  64
-// experts of 7168 x 4096 with 120 rows each took 404 us on N and 438 on M;
-// 80 rows 375 and 434.
+// experts of 7168 x 4096 with 120 rows each took 397 us on N and 503 on M;
+// 80 rows 360 and 488.
 constexpr int kRowsOnM = 129;
 static_assert(kRowsOnM <= 129, "a batch of two blocks has 128 columns each");
 // Registers: 384 x 168 at launch; the accumulating warps take what the
@@ -104,7 +105,7 @@ __device__ __forceinline__ Unit unit_of(int u, const int* offs, const int* prefi
   x.row0 = t.row0;
   x.n_valid = t.n_valid;
   x.rows_m = !FEW && x.n_valid >= kRowsOnM;
-  x.n_mma = x.rows_m ? Tile<FEW>::ROWS : (x.n_valid + 31) / 32 * 32;  // (two boxes of at least 16)
+  x.n_mma = x.rows_m ? Tile<FEW>::ROWS : (x.n_valid + 31) / 32 * 32;
   x.batch = x.rows_m ? 1 : FEW || x.n_mma <= 64 ? 4 : 2;
   return x;
 }
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
-      ptx::mbar_init(empty_bar(s), 2);  // both CTAs' MMAs: either producer writes into both
+      ptx::mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf_bar(b), 1);
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
   }
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&maps.w);
-    for (int i = 0; i < 4; ++i) ptx::prefetch_tmap(&maps.a[i]);
+    for (int i = T::BOX0; i < T::BOXES; ++i) ptx::prefetch_tmap(&maps.a[i]);
   }
   if (warp == 1) {
     ptx::tmem_alloc<false>(ptx::smem_u32(tmem_slot), 512);
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
 
   row_tiles<kBN>(p, offs, prefix, kThreads);
   ptx::tc_fence_before();
-  ptx::cluster_sync();  // (also: the peer's barriers are initialised)
+  __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int units = prefix[p.E] * p.MT;
@@ -291,15 +292,18 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
       bool ok = true;
       for (int u = u_first; u < units && ok; u += u_step) {
         const Unit x = unit_of<FEW>(u, offs, prefix, p.E, p.MT);
-        // shared rows come in two boxes of 16, 32, 64 or 128 rows, one from each CTA
-        const int half = x.n_mma / 2;
-        const int box = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+        // rows on M: this CTA's 128 rows, both halves of the channels; rows on N:
+        // all rows, this CTA's 128 channels.  The box holds the rows and few
+        // more (one row on each of 8 experts of 7168 x 4096: 63 us with 32,
+        // 48 with 16, 46 with 8); what the MMA reads past it is any earlier
+        // block's, in columns that nobody stores.
+        int box = T::BOX0;
+        while (box < 4 && x.n_valid > 8 << box) ++box;
         const CUtensorMap* am = &maps.a[box];
-        const uint32_t shared_rows = x.rows_m ? 256u : 32u << box, bytes = kOwnBytes + shared_rows * 128u;
-        const uint32_t w_at = x.rows_m ? kOwnBytes + rank * 16384u : 0u;
-        const uint32_t r_at = x.rows_m ? 0u : kOwnBytes + rank * (2048u << box);
-        const int ch = x.mt * 256 + (int)rank * 128, row = x.row0 + (int)rank * (16 << box);
-        const uint64_t pol = x.tiles > 1 ? keep : once;
+        const uint32_t bytes = kOwnBytes + (x.rows_m ? 256u : 8u << box) * 128u;
+        const int ch = x.mt * 256 + (x.rows_m ? 0 : (int)rank * 128), row = x.row0 + (x.rows_m ? (int)rank * 128 : 0);
+        // (weights that the pair reads twice, or another unit again, stay in L2)
+        const uint64_t pol = x.rows_m || x.tiles > 1 ? keep : once;
         for (int kb = 0; kb < p.KB; ++kb) {
           const int stage = base + kb % kGroup;
           if (!ptx::mbar_wait_bounded(empty_bar(stage), ((used >> stage) & 1u) ^ 1u, deadline, abort_flag)) {
@@ -307,15 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
             break;
           }
           const uint32_t sa = sbase + stage * kStageBytes, fb = full_bar(stage);
-          const int c0 = TRANS ? ch : kb * 128, c1 = TRANS ? kb * 128 : ch;
           ptx::mbar_arrive_expect_tx(fb, bytes);
-          if (x.rows_m) {
-            ptx::tma_load_2d(sa, am, fb, kb * 128, row, keep);
-            ptx::tma_load_box3_cast(sa + w_at, &maps.w, fb, c0, c1, x.g, 3, pol);
-          } else {
-            ptx::tma_load_box3(sa, &maps.w, fb, c0, c1, x.g, pol);
-            ptx::tma_load_2d_cast(sa + r_at, am, fb, kb * 128, row, 3, keep);
-          }
+          ptx::tma_load_2d(x.rows_m ? sa : sa + kOwnBytes, am, fb, kb * 128, row, keep);
+          const uint32_t wa = x.rows_m ? sa + kOwnBytes : sa;
+          ptx::tma_load_box3(wa, &maps.w, fb, TRANS ? ch : kb * 128, TRANS ? kb * 128 : ch, x.g, pol);
+          if (x.rows_m)
+            ptx::tma_load_box3(wa + kOwnBytes, &maps.w, fb, TRANS ? ch + 128 : kb * 128, TRANS ? kb * 128 : ch + 128, x.g,
+                               pol);
           used ^= 1u << stage;
           if (kb % kGroup == kGroup - 1 || kb == p.KB - 1) base = (base + kGroup) % kStages;
         }
@@ -325,8 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
         ok = ptx::mbar_wait_bounded(empty_bar(j), ((used >> j) & 1u) ^ 1u, deadline, abort_flag);
       if (!ok) {
         set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
-        // let issued copies land before shared memory is released (the peer's
-        // half of a slot may never come: the limit ends the wait)
+        // let issued copies land before shared memory is released
         const uint64_t grace = ptx::globaltimer_ns() + 100000000ull;
         for (int j = 0; j < kStages; ++j)
           while (!ptx::mbar_try_wait(full_bar(j), ((used >> j) & 1u) ^ 1u) && ptx::globaltimer_ns() < grace) {
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
             ptx::mma_f8_one<true>(one, d, da + 2 * astep, db + 2 * bstep, idesc);
             ptx::mma_f8_one<true>(one, d, da + 3 * astep, db + 3 * bstep, idesc);
             if (last) ptx::mma_commit_one(one, accf_bar(b));
-            ptx::mma_commit_cast_one(one, empty_bar(slot), 3);
+            ptx::mma_commit_one(one, empty_bar(slot));
             // (only within the unit: the next one may use the buffers in another way)
             seen = j + 1 < n ? polled(base, j + 1) : kb0 + kGroup < p.KB && polled((base + kGroup) % kStages, 0);
             any = true;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_kernel(const Params p,
 
   __syncwarp();
   ptx::tc_fence_before();
-  ptx::cluster_sync();
+  __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc<false>(tmem_base, 512);
@@ -568,20 +569,24 @@ moe_status block_gemm_launch(const BlockGemmArgs& a, cudaStream_t s) {
   p.timeout_ns = a.timeout_ns;
   if (((long long)a.R / Tile<true>::ROWS + a.E) * p.MT > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
   const bool many = (long long)a.R >= kManyRows * a.E;
+  // Few rows an expert on average (a group of more than 64 rows then takes
+  // several tiles, whose weights come from L2 again).  64 experts of 7168 x
+  // 4096 with about 40 rows each: 297 us in tiles of 64, 329 in tiles of 256.
+  // The average does not see how the rows lie: 45 on average with half of the
+  // experts empty 266 and 185, 40 with most of them on one expert 220 and 162.
+  const bool few = !many && (a.R <= 64 || (long long)a.R <= 48ll * a.E);
   const int channels = many ? 64 : 128;  // of a weight box
   Maps maps;
   if (a.transposed)
     MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.K, a.N, a.N, 1, 128, channels, channels));
   else
     MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.N, a.K, a.K, 1, channels, 128, 128));
-  for (int i = many ? 3 : 0; i < 4; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K, 1, 16u << i, 128, 128));
+  const int box0 = many ? 4 : few ? Tile<true>::BOX0 : Tile<false>::BOX0;
+  const int boxes = few ? Tile<true>::BOXES : Tile<false>::BOXES;
+  for (int i = box0; i < boxes; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K, 1, 8u << i, 128, 128));
   const int es = a.out_f32 ? 4 : 2;
   MOE_TRY(make_tmap_2d(&maps.out, a.out, a.R, a.N, es, 32, 64 / es, 64));
   if (many) return block_gemm_many_launch(p, maps, a.transposed, a.num_sms, s);
-  // Few rows an expert on average (a group of more than 64 rows then takes
-  // several tiles, whose weights come from L2 again).  64 experts of 7168 x
-  // 4096 with 40 rows each: 303 us in tiles of 64, 349 in tiles of 256.
-  const bool few = a.R <= 64 || (long long)a.R <= 48ll * a.E;
   if (few) return a.transposed ? launch<true, true>(p, maps, a.num_sms, s) : launch<false, true>(p, maps, a.num_sms, s);
   return a.transposed ? launch<true, false>(p, maps, a.num_sms, s) : launch<false, false>(p, maps, a.num_sms, s);
 }

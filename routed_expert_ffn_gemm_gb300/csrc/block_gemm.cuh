@@ -26,7 +26,7 @@ struct Params {
 
 struct Maps {
   CUtensorMap w;     // 128 of the reduction x 128 channels (block_gemm_many.cu: 64)
-  CUtensorMap a[4];  // boxes of 16, 32, 64, 128 rows
+  CUtensorMap a[5];  // boxes of 8 << i rows
   CUtensorMap out;   // 32 rows of 64 bytes
 };
 
@@ -195,9 +195,11 @@ moe_status launch_clusters(Kernel kern, std::atomic<int> (&known)[64], int smem,
 
 // From this many rows an expert on average the product runs on
 // block_gemm_many.cu.  64 experts of 7168 x 4096, us there and in
-// block_gemm.cu: 80 rows 396 and 375, 100 rows 397 and 404, 120 rows 391 and
-// 403, 160 rows 393 and 429; 90 rows unevenly spread 417 and 389; one expert
-// with 100 rows 31 and 34.
+// block_gemm.cu: 80 rows 379 and 358, 100 rows 381 and 394, 120 rows 385 and
+// 395, 160 rows 386 and 437; 90 rows unevenly spread 401 and 377; one expert
+// with 100 rows 31 and 35.  The average counts experts without rows, which
+// the host cannot see: 90 rows on average with half of the experts empty 198
+// and 224.
 constexpr long long kManyRows = 100;
 moe_status block_gemm_many_launch(const block_gemm::Params& p, const block_gemm::Maps& maps, bool transposed,
                                   int num_sms, cudaStream_t s);

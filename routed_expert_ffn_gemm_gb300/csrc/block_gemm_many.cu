@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
   }
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&maps.w);
-    ptx::prefetch_tmap(&maps.a[3]);
+    ptx::prefetch_tmap(&maps.a[4]);
     ptx::prefetch_tmap(&maps.out);
   }
   if (warp == 1) {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_gemm_many_kernel(const Para
           }
           const uint32_t at = sbase + s * kStageBytes, fb = lead(full_bar(s));
           ptx::mbar_arrive_expect_tx_cluster(fb, kStageBytes);
-          ptx::tma_load_2d_pair(at, &maps.a[3], fb, kb * 128, row, keep);
+          ptx::tma_load_2d_pair(at, &maps.a[4], fb, kb * 128, row, keep);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             ptx::tma_load_box3_pair(at + kTileBytes + h * kHalfBytes, &maps.w, fb, TRANS ? ch + 128 * h : kb * 128,

@@ -253,25 +253,6 @@ __device__ __forceinline__ void tma_load_box3_pair(uint32_t dst, const CUtensorM
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
-// The same into the shared memory of every CTA of the cluster whose bit is set
-// in `mask`, at the same offset, completing the barrier at `bar`'s offset in
-// each of them.
-__device__ __forceinline__ void tma_load_box3_cast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0,
-                                                   int32_t c1, int32_t c2, uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6, %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "h"(mask), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_cast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c_inner,
-                                                 int32_t c_outer, uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c_inner), "r"(c_outer), "h"(mask), "l"(policy)
-      : "memory");
-}
 
 // Store (or add) of a box from this CTA's shared memory at coordinates inside
 // the map; it belongs to this thread's bulk group.
@@ -460,16 +441,6 @@ __device__ __forceinline__ void mma_commit_one(uint32_t one, uint32_t bar) {
       "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit_cast_one(uint32_t one, uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::
-          "r"(bar),
-      "h"(mask), "r"(one)
-      : "memory");
-}
-
 __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(

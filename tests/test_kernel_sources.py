@@ -36,3 +36,21 @@ def test_cluster_has_started_before_its_memory_is_written():
     kernel = text[text.index("    router_losses_sum_kernel("):]
     before = kernel[: kernel.index("st.shared::cluster")]
     assert "cluster_sync();" in before or before.index("cluster_arrive();") < before.index("cluster_wait();")
+
+
+def statements(path):
+    """The instructions of each asm statement of a source file."""
+    with open(path) as f:
+        text = f.read()
+    for body in re.findall(r"\basm(?:\s+volatile)?\s*\((.*?)\);", text, re.S):
+        yield "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', body))
+
+
+def test_copies_are_found():
+    assert SOURCES and any("cp.async.bulk.tensor" in s for p in SOURCES for s in statements(p))
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=[os.path.basename(p) for p in SOURCES])
+def test_no_copy_is_multicast(path):
+    # the library is also loaded by replicas on several GPUs
+    assert not [s for s in statements(path) if "cp.async.bulk" in s and "multicast" in s]
