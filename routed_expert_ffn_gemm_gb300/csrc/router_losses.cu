@@ -18,6 +18,8 @@
 // atomics, so every run gives the same bits.
 #include <math.h>
 
+#include <atomic>
+
 #include "ptx.cuh"
 #include "train.cuh"
 
@@ -377,9 +379,20 @@ template <int LG, int VEC, int NI>
 struct Forward {
   static moe_status run(const RouterLossArgs& a, int blocks, cudaStream_t s) {
     constexpr int THREADS = forward_threads(NI * VEC);
+    constexpr int MOST = LG * VEC * NI;  // experts of this layout
     const size_t smem = 4 * (size_t)(THREADS / 32 + 1) * a.E;
     auto kern = router_losses_kernel<LG, VEC, NI, THREADS>;
-    MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    // The limit belongs to the function, not to the launch: it is raised once
+    // to what the layout's widest rows take, since a call that set its own
+    // size could take it from another thread's between its setting and launch.
+    static std::atomic<bool> raised[64];
+    int dev = 0;
+    MOE_TRY_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    if (!raised[dev].load(std::memory_order_relaxed)) {
+      MOE_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (THREADS / 32 + 1) * MOST));
+      raised[dev].store(true, std::memory_order_relaxed);
+    }
     MOE_TRY_CUDA(launch_k(kern, dim3(blocks), dim3(THREADS), smem, s, a));
     return MOE_OK;
   }

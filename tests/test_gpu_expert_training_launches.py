@@ -2,6 +2,8 @@
 time on the current stream: in quick succession, on given streams, from
 several threads, on results past 2^31 elements."""
 
+import threading
+
 import pytest
 import torch
 
@@ -57,3 +59,35 @@ def test_router_sum_with_idle_ctas(E, k):
     assert torch.equal(runs[0].counts.cpu(), want[2])
     for r in runs:
         assert torch.equal(r.loss, runs[0].loss) and torch.equal(r.counts, runs[0].counts)
+
+
+def test_router_losses_from_two_threads():
+    # both sizes run the same kernel, with 52 800 and 67 584 bytes of shared
+    # memory: a call's launch must not depend on another thread's calls
+    T, k, errors = 200, 4, []
+
+    def work(E):
+        try:
+            logits, idx, _ = routed(T, E, k, seed=E)
+            want = ref.router(logits.double(), idx, None, 0.3, 0.02)
+            logits, idx = logits.to(DEV), idx.to(DEV)
+            r = api.router_losses(logits, idx, 0.3, 0.02)
+            ws = torch.empty(api.moe_router_losses_workspace_size(T, E), dtype=torch.uint8, device=DEV)
+            args = (T, E, k, logits.data_ptr(), idx.data_ptr(), None, 0.3, 0.02, r.loss.data_ptr(), r.counts.data_ptr(),
+                    r.lse.data_ptr(), ws.data_ptr(), ws.numel(), api._stream(None))
+            start.wait(timeout=60)
+            for _ in range(20000):
+                api._call("moe_router_losses", *args)
+            torch.cuda.synchronize()
+            close(r.loss, torch.stack(want[:2]))
+        except Exception as e:  # (an assertion in a thread would be lost)
+            errors.append(f"E = {E}: {e!r}")
+            start.abort()
+
+    start = threading.Barrier(2)
+    threads = [threading.Thread(target=work, args=(E,), daemon=True) for E in (400, 512)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    assert not errors and not any(t.is_alive() for t in threads)
