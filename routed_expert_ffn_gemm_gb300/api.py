@@ -203,6 +203,23 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on_stream(stream, fn, *args):
+    """fn(*args) with `stream` current, for calls that allocate or copy: what
+    they make is ordered with their kernels and not reused before those end.
+    Results are also kept from reuse until the stream that is current here has
+    done what it was given by the time they are dropped."""
+    here = torch.cuda.current_stream()
+    if stream.cuda_stream == here.cuda_stream:
+        return fn(*args)
+    given = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(given):
+        out = fn(*args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if isinstance(t, torch.Tensor):
+            t.record_stream(here)
+    return out
+
+
 def _call(name, *args):
     st = getattr(_lib(), name)(*args)
     if st != OK:
@@ -483,6 +500,8 @@ def _pitched(t: torch.Tensor) -> int:
 def quantize_blocks(x, scale="amax", codes=None, scales=None, stream=None):
     """moe_quantize_blocks_e4m3 of the rows of x [..., cols] (a matrix's rows
     may lie apart): (codes uint8 [..., cols], scales fp32 [..., blocks])."""
+    if stream is not None:
+        return _on_stream(stream, quantize_blocks, x, scale, codes, scales)
     if scale not in SCALE:
         raise ValueError(f"scale: {scale!r}, the call takes {sorted(SCALE)}")
     kind, shape, dev = _type(x.dtype, "x"), x.shape, x.device
@@ -498,7 +517,7 @@ def quantize_blocks(x, scale="amax", codes=None, scales=None, stream=None):
     else:
         _exact(scales, "scales", sshape, torch.float32)
     _call("moe_quantize_blocks_e4m3", m.shape[0], cols, kind, SCALE[scale], _pitched(m), ld, _ptr(codes), _ptr(scales),
-          _stream(stream))
+          _stream(None))
     return codes, scales
 
 

@@ -91,3 +91,37 @@ def test_router_losses_from_two_threads():
     for t in threads:
         t.join(timeout=120)
     assert not errors and not any(t.is_alive() for t in threads)
+
+
+# What a call with stream= reads is made on that stream behind some 50 ms of
+# waiting, and the current stream meanwhile fills every freed block with other
+# values: a copy, a buffer or a launch on the current stream shows.
+
+def values_of(out):
+    return [t for t in (out if isinstance(out, tuple) else (out,)) if isinstance(t, torch.Tensor)]
+
+
+def check_on_stream(fn, tensors):
+    """fn(tensors, **kw) with stream=side against the same call without."""
+    want = [t.clone() for t in values_of(fn(tensors))]
+    sizes = sorted({t.numel() * t.element_size() for t in want} | {1 << p for p in range(9, 22)})
+    later = [None if t is None else torch.zeros_like(t) for t in tensors]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        for t, v in zip(later, tensors):
+            if t is not None:
+                t.copy_(v)
+    got = fn(later, stream=side)
+    churn = [torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(8)]
+    del churn
+    side.synchronize()
+    got = values_of(got)
+    assert len(got) == len(want) and all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("shape,axes", [((300, 256), None), ((40, 30, 384), (1, 0, 2)), ((96, 128, 5), (2, 0, 1))])
+def test_quantize_blocks_on_a_given_stream(shape, axes):
+    x = normal(*shape, seed=3).to(DEV)
+    check_on_stream(lambda t, **kw: api.quantize_blocks(t[0] if axes is None else t[0].permute(axes), "pow2", **kw), [x])
