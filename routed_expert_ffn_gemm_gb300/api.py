@@ -435,6 +435,8 @@ def workspace_for(p, device="cuda") -> torch.Tensor:
 def layer_forward(p, case, out=None, workspace=None, want_routing=False, stream=None, timer=None):
     """moe_layer_forward (or moe_layer_forward_timed when a StageTimer is
     given) on a case dict (``inputs.make_case`` keys)."""
+    if stream is not None:
+        return _on_stream(stream, layer_forward, p, case, out, workspace, want_routing, None, timer)
     x = case["x"]
     if out is None:
         out = torch.empty_like(x)
@@ -450,9 +452,9 @@ def layer_forward(p, case, out=None, workspace=None, want_routing=False, stream=
             case["w_shared_gate"], case["w_shared_up"], case["w_shared_down"], out,
             idx, w, counts, workspace)
     if timer is None:
-        moe_layer_forward(*args, stream=stream)
+        moe_layer_forward(*args)
     else:
-        moe_layer_forward_timed(*args, timer, stream=stream)
+        moe_layer_forward_timed(*args, timer)
     return (out, idx, w, counts) if want_routing else out
 
 
@@ -525,6 +527,8 @@ def grouped_block_gemm(a, a_scales, offsets, w, w_scales, transposed=False, out_
                        stream=None):
     """moe_grouped_block_gemm: rows a [R, K] (codes) of each expert times its
     w [E, N, K] (transposed: [E, K, N]) -> [R, N]."""
+    if stream is not None:
+        return _on_stream(stream, grouped_block_gemm, a, a_scales, offsets, w, w_scales, transposed, out_dtype, out)
     if a.dim() != 2 or w.dim() != 3:
         raise ValueError("a: [R, K] and w: [E, N, K] are expected")
     R, K = a.shape
@@ -541,7 +545,7 @@ def grouped_block_gemm(a, a_scales, offsets, w, w_scales, transposed=False, out_
     _exact(w_scales, "w_scales", sshape, torch.float32)
     _exact(out, "out", (R, N), out.dtype)
     _call("moe_grouped_block_gemm", R, K, N, E, int(bool(transposed)), kind, _ptr(a), _ptr(a_scales), _ptr(offsets),
-          _ptr(w), _ptr(w_scales), _ptr(out), _stream(stream))
+          _ptr(w), _ptr(w_scales), _ptr(out), _stream(None))
     return out
 
 
@@ -567,6 +571,8 @@ class SwigluGrads(NamedTuple):
 def swiglu_save(g, u, want_h=False, want_codes=True, stream=None) -> SwigluSaved:
     """moe_swiglu_save_e4m3 of g and u [R, ffn] bf16 (for instance the halves
     of one product's rows)."""
+    if stream is not None:
+        return _on_stream(stream, swiglu_save, g, u, want_h, want_codes)
     ld = _rows(g, "g", torch.bfloat16)
     if _rows(u, "u", torch.bfloat16) != ld or u.shape != g.shape:
         raise ValueError("g and u: two matrices of one shape and row pitch are expected")
@@ -577,12 +583,14 @@ def swiglu_save(g, u, want_h=False, want_codes=True, stream=None) -> SwigluSaved
     saved = torch.empty((2, R, f), dtype=torch.uint8, device=dev)
     saved_scales = torch.empty((2, R, nb), dtype=torch.float32, device=dev)
     _call("moe_swiglu_save_e4m3", R, f, _pitched(g), _pitched(u), ld, _ptr(h), _ptr(codes), _ptr(scales), _ptr(saved),
-          _ptr(saved_scales), _stream(stream))
+          _ptr(saved_scales), _stream(None))
     return SwigluSaved(h, codes, scales, saved, saved_scales)
 
 
 def swiglu_backward(saved, saved_scales, dh, want_h=False, want_codes=False, stream=None) -> SwigluGrads:
     """moe_swiglu_backward_e4m3 of what swiglu_save kept and dh [R, ffn] bf16."""
+    if stream is not None:
+        return _on_stream(stream, swiglu_backward, saved, saved_scales, dh, want_h, want_codes)
     if dh.dim() != 2:
         raise ValueError("dh: [R, ffn] is expected")
     R, f = dh.shape
@@ -595,13 +603,15 @@ def swiglu_backward(saved, saved_scales, dh, want_h=False, want_codes=False, str
     scales = torch.empty((R, _blocks(2 * f)), dtype=torch.float32, device=dh.device) if want_codes else None
     dg = _ptr(d_gu)
     _call("moe_swiglu_backward_e4m3", R, f, _ptr(saved), _ptr(saved_scales), _ptr(dh), dg,
-          dg + 2 * f if dg else None, 2 * f, _ptr(h), _ptr(codes), _ptr(scales), _stream(stream))
+          dg + 2 * f if dg else None, 2 * f, _ptr(h), _ptr(codes), _ptr(scales), _stream(None))
     return SwigluGrads(d_gu, h, codes, scales)
 
 
 def grouped_wgrad(dy, x, x_scales, offsets, dw=None, accumulate=False, dw_dtype=torch.float32, stream=None):
     """moe_grouped_wgrad: dw [E, N, K] of dy [R, N] bf16 (its rows may lie
     apart) and x [R, K], bf16 (x_scales None) or codes with their scales."""
+    if stream is not None:
+        return _on_stream(stream, grouped_wgrad, dy, x, x_scales, offsets, dw, accumulate, dw_dtype)
     ld = _rows(dy, "dy", torch.bfloat16)
     R, N = dy.shape
     K, E = x.shape[-1], offsets.numel() - 1
@@ -615,7 +625,7 @@ def grouped_wgrad(dy, x, x_scales, offsets, dw=None, accumulate=False, dw_dtype=
     kind = _type(dw.dtype, "dw")
     _exact(dw, "dw", (E, N, K), dw.dtype)
     _call("moe_grouped_wgrad", R, N, K, E, DTYPE["bf16" if x_scales is None else "fp8"], kind, int(bool(accumulate)),
-          _pitched(dy), ld, _ptr(x), _ptr(x_scales), _ptr(offsets), _ptr(dw), _stream(stream))
+          _pitched(dy), ld, _ptr(x), _ptr(x_scales), _ptr(offsets), _ptr(dw), _stream(None))
     return dw
 
 
@@ -660,6 +670,8 @@ def _check_router(logits, idx, mask):
 
 def router_losses(logits, topk_idx, balance, z, mask=None, workspace=None, stream=None) -> RouterLosses:
     """moe_router_losses of logits [T, E] and the chosen experts [T, k]."""
+    if stream is not None:
+        return _on_stream(stream, router_losses, logits, topk_idx, balance, z, mask, workspace)
     T, E, k = _check_router(logits, topk_idx, mask)
     dev = logits.device
     loss = torch.empty(2, dtype=torch.float32, device=dev)
@@ -668,7 +680,7 @@ def router_losses(logits, topk_idx, balance, z, mask=None, workspace=None, strea
     if workspace is None:
         workspace = torch.empty(_router_workspace(T, E, torch._C._cuda_getDevice()), dtype=torch.uint8, device=dev)
     _call("moe_router_losses", T, E, k, _ptr(logits), _ptr(topk_idx), _ptr(mask), balance, z, _ptr(loss), _ptr(counts),
-          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+          _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(None))
     return RouterLosses(loss, counts, lse, balance, z)
 
 
@@ -676,6 +688,8 @@ def router_losses_backward(logits, topk_idx, losses: RouterLosses, grad=None, to
                            stream=None):
     """moe_router_losses_backward: the gradient of the logits [T, E]; grad is
     a device scalar (None: 1)."""
+    if stream is not None:
+        return _on_stream(stream, router_losses_backward, logits, topk_idx, losses, grad, topk_w, d_topk_w, mask)
     T, E, k = _check_router(logits, topk_idx, mask)
     _exact(losses.counts, "counts", (E + 1,), torch.int32)
     _exact(losses.lse, "lse", (T,), torch.float32)
@@ -685,5 +699,5 @@ def router_losses_backward(logits, topk_idx, losses: RouterLosses, grad=None, to
     d_logits = torch.empty_like(logits)
     _call("moe_router_losses_backward", T, E, k, _ptr(logits), _ptr(topk_idx), _ptr(mask), losses.balance, losses.z,
           _ptr(losses.counts), _ptr(losses.lse), _ptr(grad), _ptr(topk_w), _ptr(d_topk_w), _ptr(d_logits),
-          _stream(stream))
+          _stream(None))
     return d_logits

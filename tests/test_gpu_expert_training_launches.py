@@ -7,7 +7,7 @@ import threading
 import pytest
 import torch
 
-from routed_expert_ffn_gemm_gb300 import api, build
+from routed_expert_ffn_gemm_gb300 import api, build, inputs
 from tests import train_reference as ref
 from tests.test_gpu_expert_training import close, gemm_case, normal, offsets_of, routed
 
@@ -125,3 +125,42 @@ def check_on_stream(fn, tensors):
 def test_quantize_blocks_on_a_given_stream(shape, axes):
     x = normal(*shape, seed=3).to(DEV)
     check_on_stream(lambda t, **kw: api.quantize_blocks(t[0] if axes is None else t[0].permute(axes), "pow2", **kw), [x])
+
+
+def test_products_and_gradients_on_a_given_stream():
+    counts, K, N = [50, 0, 120], 256, 384
+    R, a, sa, off, w, sw = gemm_case(counts, 0, 0, K, N, False, seed=6)
+    a, sa, off, w, sw = (t.to(DEV) for t in (a, sa, off, w, sw))
+    check_on_stream(lambda t, **kw: api.grouped_block_gemm(*t, **kw), [a, sa, off, w, sw])
+    dy = normal(R, N, seed=7).to(DEV)
+    check_on_stream(lambda t, **kw: api.grouped_wgrad(*t, **kw), [dy, a, sa, off])
+    check_on_stream(lambda t, **kw: api.grouped_wgrad(t[0], t[1], None, t[2], t[3].clone() if not kw else t[3], True, **kw),
+                    [dy, normal(R, K, seed=8).to(DEV), off, torch.ones(3, N, K, device=DEV)])
+
+
+def test_swiglu_on_a_given_stream():
+    gu, dh = normal(333, 512, seed=9).to(DEV), normal(333, 256, seed=10).to(DEV)
+    check_on_stream(lambda t, **kw: api.swiglu_save(t[0][:, :256], t[0][:, 256:], want_h=True, **kw), [gu])
+    saved, scales = api.quantize_blocks(gu.view(333, 2, 256).transpose(0, 1), "pow2")
+    check_on_stream(lambda t, **kw: api.swiglu_backward(*t, want_h=True, want_codes=True, **kw), [saved, scales, dh])
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 8, 2), (5000, 60, 4)])
+def test_router_on_a_given_stream(T, E, k):
+    # (the workspace that the call makes for itself among what must not be reused)
+    logits, idx, w = (t.to(DEV) for t in routed(T, E, k, seed=1))
+    check_on_stream(lambda t, **kw: tuple(api.router_losses(t[0], t[1], 0.3, 0.02, **kw))[:3], [logits, idx])
+    r = api.router_losses(logits, idx, 0.3, 0.02)
+    check_on_stream(lambda t, **kw: api.router_losses_backward(
+        t[0], t[1], api.RouterLosses(t[2], t[3], t[4], 0.3, 0.02), topk_w=t[5], d_topk_w=t[5], **kw),
+        [logits, idx, r.loss, r.counts, r.lse, w])
+
+
+@pytest.mark.parametrize("wfmt", ["bf16", "fp8"])
+def test_layer_forward_on_a_given_stream(wfmt):
+    shape = inputs.MoEShape("stream", T=40, d=256, ffn=384, E=8, k=2, ffn_shared=256, wfmt=wfmt)
+    case = inputs.make_case(shape, seed=4, device=DEV)
+    names = sorted(case, key=str)
+    names = [n for n in names if isinstance(case[n], torch.Tensor)]
+    check_on_stream(lambda t, **kw: api.layer_forward(api.problem_of(shape), dict(case, **dict(zip(names, t))),
+                                                      want_routing=True, **kw), [case[n] for n in names])

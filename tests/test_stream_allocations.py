@@ -69,3 +69,39 @@ def check(monkeypatch, fn, args):
 @pytest.mark.parametrize("x", [b16(6, 128), b16(3, 2, 128).transpose(0, 1), b16(128)], ids=["matrix", "copied", "row"])
 def test_quantize_blocks(monkeypatch, x):
     check(monkeypatch, api.quantize_blocks, (x,))
+
+
+def u8(*s):
+    return torch.zeros(*s, dtype=torch.uint8)
+
+
+def i32(*s):
+    return torch.zeros(*s, dtype=torch.int32)
+
+
+f32 = torch.zeros
+LOSSES = api.RouterLosses(f32(2), i32(9), f32(6), 1.0, 1.0)
+
+
+@pytest.mark.parametrize("fn,args", [
+    (api.grouped_block_gemm, (u8(6, 144), f32(6, 2), i32(3), u8(2, 272, 144), f32(2, 3, 2))),
+    (api.swiglu_save, (b16(6, 144), b16(6, 144), True)),
+    (api.swiglu_backward, (u8(2, 6, 128), f32(2, 6, 1), b16(6, 128), True, True)),
+    (api.grouped_wgrad, (b16(6, 144), u8(6, 272), f32(6, 3), i32(3))),
+    (api.router_losses, (f32(6, 8), i32(6, 2), 1.0, 1.0)),
+    (api.router_losses_backward, (f32(6, 8), i32(6, 2), LOSSES))])
+def test_training_operators(monkeypatch, fn, args):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(api, "_router_workspace", lambda *a: 64)
+    check(monkeypatch, fn, args)
+
+
+@pytest.mark.parametrize("want_routing", [False, True])
+def test_layer_forward(monkeypatch, want_routing):
+    monkeypatch.setattr(api, "moe_workspace_size", lambda p: 64)
+    monkeypatch.setattr(api, "_check_layer", lambda *a: None)
+    p = api.problem(6, 128, 128, 4, 2)
+    names = ("w_router", "router_bias", "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down", "w_shared_gate",
+             "w_shared_up", "w_shared_down")
+    case = dict({n: None for n in names}, x=b16(6, 128))
+    check(monkeypatch, api.layer_forward, (p, case, None, None, want_routing))
