@@ -315,15 +315,22 @@ __global__ void __launch_bounds__(kThreads) router_losses_backward_kernel(const 
       }
       __syncwarp();
     }
+    // Probabilities are the terms over their own sum: lse is rounded to fp32,
+    // by 2^-25 of its magnitude, and exp(l - lse) alone would be off by that
+    // (by 5e-4 where the logits are about 8000).
     const bool some = live && lse != -INFINITY;
-    float fp = 0.f;
+    float fp = 0.f, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NI * VEC; ++i) {
       const int e = Row<LG, VEC, NI>::col(i / VEC, l) + i % VEC;
       r.v[i] = some ? __expf(r.v[i] - lse) : 0.f;
+      sum += r.v[i];
       if (e < a.E) fp = fmaf(f[e], r.v[i], fp);
     }
     fp = group_sum<LG>(fp);
+    sum = group_sum<LG>(sum);
+    const float inv = 1.f / sum, scale = up * inv;  // (sum 0 where nothing uses them)
+    fp *= inv;
     const float zt = some ? cz * lse : 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -332,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) router_losses_backward_kernel(const 
       float d[VEC];
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
-        d[c] = some ? up * (r.v[i * VEC + c] * fmaf(cb, f[e0 + c] - fp, zt)) : 0.f;
+        d[c] = some ? scale * (r.v[i * VEC + c] * fmaf(cb, f[e0 + c] - fp, zt)) : 0.f;
         if (a.w != nullptr) d[c] += add[e0 + c];
       }
       float* to = a.dlogits + (size_t)t * a.E + e0;
