@@ -37,3 +37,43 @@ def test_router_gradient_of_shifted_logits(T, E, k, shift, balance, z):
     r = api.router_losses(logits, idx, balance, z)
     close(r.loss, torch.stack([lb, lz]).detach())
     close(api.router_losses_backward(logits, idx, r), l64.grad)
+
+
+def gates(lo=-65.0, hi=20.0, rows=256):
+    """Rows of 128 equal gates, bf16 values from lo to hi."""
+    g = torch.linspace(lo, hi, rows).bfloat16()
+    return g[:, None].expand(rows, 128).contiguous()
+
+
+# an fp32 operation is off by half a unit of 2^-23 at most, expf and the
+# approximate reciprocal by two and one, as CUDA's tables state
+
+def test_swiglu_scales_follow_the_gate():
+    # sigmoid 2 + 0.5 + 1, two products 0.5 each, the division by 448 0.5
+    g = gates()
+    r = api.swiglu_save(g.to(DEV), torch.ones_like(g).to(DEV))
+    want = (g[:, :1].double() * torch.sigmoid(g[:, :1].double())).abs() / 448
+    assert ((r.scales.cpu().double() - want).abs() <= 6 * 2.0 ** -23 * want)[want > 0].all()
+
+
+def test_swiglu_gradient_scales_follow_the_gate():
+    # du: as above.  dg: the sigmoid's 3.5; 1 + g (1 - s) 0.5 three times, at
+    # most doubled where the addition cancels (|g| >= 2); three products and
+    # the division
+    g = gates(-60.0, -2.0)
+    saved, scales = ref.quantize(torch.stack([g, torch.ones_like(g)]), "pow2")
+    r = api.swiglu_backward(saved.to(DEV), scales.to(DEV), torch.ones_like(g).to(DEV), want_codes=True)
+    v = ref.widen(saved, scales)[0, :, :1]
+    s = torch.sigmoid(v)
+    want = torch.cat([s * (1 + v * (1 - s)), v * s], 1).abs() / 448
+    assert ((r.scales.cpu().double() - want).abs() <= torch.tensor([9.0, 6.0]) * 2.0 ** -23 * want).all()
+
+
+def test_swiglu_of_infinite_and_nan_gates():
+    inf, nan = float("inf"), float("nan")
+    g = torch.tensor([inf, -inf, nan, 3e38, -3e38, 0.0, -0.0, 1.0] * 16).bfloat16()[None]
+    r = api.swiglu_save(g.to(DEV), torch.ones_like(g).to(DEV), want_h=True)
+    want = ref.silu_mul(g.double(), torch.ones_like(g).double()).bfloat16()
+    got = r.h.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert ((got == want) | torch.isnan(want) | ((got - want).abs() <= 2.0 ** -8 * want.abs())).all()
