@@ -157,16 +157,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
-// Bounded wait for two barriers' phases (both polled at once: a poll takes
-// about 90 cycles even when the phase is complete).
-__device__ __forceinline__ bool mbar_wait2_bounded(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b,
-                                                   uint32_t parity_b, uint64_t deadline_ns, volatile int* abort) {
-  const bool a = mbar_try_wait(bar_a, parity_a), b = mbar_try_wait(bar_b, parity_b);
-  if (a && b) return true;
-  return (a || mbar_wait_bounded(bar_a, parity_a, deadline_ns, abort)) &&
-         (b || mbar_wait_bounded(bar_b, parity_b, deadline_ns, abort));
-}
-
 // ---------------------------------------------------------------------------
 // TMA
 // ---------------------------------------------------------------------------
@@ -497,15 +487,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       : "memory");
 }
 
-// The commit of this CTA's own operations, arriving on the barrier at offset
-// `bar` in every CTA of `mask`.
-__device__ __forceinline__ void mma_commit_cast(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
-}
-
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far
 // has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -535,7 +516,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
-// Two fp32 values in a 64-bit register, and their fused multiply-add.
+// Two fp32 values in a 64-bit register, their products and sums.
 __device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
   uint64_t v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
@@ -544,12 +525,6 @@ __device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
