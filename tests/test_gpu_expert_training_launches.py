@@ -9,7 +9,7 @@ import torch
 
 from routed_expert_ffn_gemm_gb300 import api, build, inputs
 from tests import train_reference as ref
-from tests.test_gpu_expert_training import close, gemm_case, normal, offsets_of, routed
+from tests.test_gpu_expert_training import close, gemm_case, gen, normal, offsets_of, routed
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -164,3 +164,72 @@ def test_layer_forward_on_a_given_stream(wfmt):
     names = [n for n in names if isinstance(case[n], torch.Tensor)]
     check_on_stream(lambda t, **kw: api.layer_forward(api.problem_of(shape), dict(case, **dict(zip(names, t))),
                                                       want_routing=True, **kw), [case[n] for n in names])
+
+
+# Results past 2^31 elements: the first and the last rows against the same
+# rows by themselves (what lies between is zero).
+
+ENDS = 40
+
+
+def ends_of(t, dim=0):
+    return torch.cat([t.narrow(dim, 0, ENDS), t.narrow(dim, t.shape[dim] - ENDS, ENDS)], dim)
+
+
+def tall(rows, cols, seed, dtype=torch.bfloat16):
+    x = torch.zeros(rows, cols, dtype=dtype, device=DEV)
+    e = normal(2 * ENDS, cols, seed=seed).to(dtype).to(DEV)
+    x[:ENDS], x[rows - ENDS:] = e[:ENDS], e[ENDS:]
+    return x, e
+
+
+def test_quantize_blocks_past_32_bits():
+    x, e = tall((1 << 20) + 77, 2056, 1)
+    assert x.numel() > 1 << 31
+    codes, scales = api.quantize_blocks(x, "pow2")
+    c, s = api.quantize_blocks(e, "pow2")
+    assert torch.equal(ends_of(codes), c) and torch.equal(ends_of(scales), s)
+    assert not codes[ENDS:-ENDS].any()
+
+
+def test_swiglu_past_32_bits():
+    f = 2064
+    gu, e = tall((1 << 20) + 77, 2 * f, 2)
+    r, w = (api.swiglu_save(t[:, :f], t[:, f:], want_h=True) for t in (gu, e))
+    assert r.h.numel() > 1 << 31
+    assert torch.equal(ends_of(r.h), w.h) and torch.equal(ends_of(r.codes), w.codes)
+    assert torch.equal(ends_of(r.saved, 1), w.saved) and torch.equal(ends_of(r.saved_scales, 1), w.saved_scales)
+    del gu
+    d, v = (api.swiglu_backward(t.saved, t.saved_scales, t.h, want_h=True) for t in (r, w))
+    assert torch.equal(ends_of(d.d_gu), v.d_gu) and torch.equal(ends_of(d.h), v.h)
+
+
+@pytest.mark.parametrize("E,R,K,N", [(3, 300_032, 128, 7168), (1024, 49_100, 16, 44_032)], ids=["many", "few"])
+def test_block_gemm_past_32_bits(E, R, K, N):
+    assert R * N > 1 << 31
+    x, e = tall(R, K, 3)
+    a, sa = api.quantize_blocks(x)
+    w, sw = ref.quantize(normal(8, N, K, seed=4), "amax")
+    w = w.repeat(E // 8 + 1, 1, 1)[:E].contiguous()
+    sw = torch.rand(E, -(-N // 128), 1, generator=gen(5)) + 0.5
+    off = torch.linspace(0, R, E + 1).round().to(torch.int32)
+    out = api.grouped_block_gemm(a, sa, off.to(DEV), w.to(DEV), sw.to(DEV))
+    first, last = int((off[1:] <= 0).sum()), E - 1
+    for rows, g in ((slice(0, min(ENDS, int(off[first + 1]))), first), (slice(max(R - ENDS, int(off[last])), R), last)):
+        n = rows.stop - rows.start
+        y, mag = ref.block_gemm(a[rows].cpu(), sa[rows].cpu(), offsets_of([n]), w[g:g + 1], sw[g:g + 1], False)
+        # (as the block product's tests have it, for one block)
+        assert ((out[rows].cpu().double() - y).abs() <= 36 * 2.0 ** -24 * mag + 2.0 ** -8 * y.abs()).all()
+
+
+def test_wgrad_past_32_bits():
+    E, N, K = 64, 8192, 4112
+    assert E * N * K > 1 << 31
+    counts = [5] + [0] * (E - 2) + [21]
+    dy, x = normal(26, N, seed=6).to(DEV), normal(26, K, seed=7).to(DEV)
+    dw = torch.full((E, N, K), 7.0, device=DEV)
+    api.grouped_wgrad(dy, x, None, offsets_of(counts).to(DEV), dw)
+    for g, rows in ((0, slice(0, 5)), (E - 1, slice(5, 26))):
+        n = rows.stop - rows.start
+        assert torch.equal(dw[g], api.grouped_wgrad(dy[rows], x[rows], None, offsets_of([n]).to(DEV))[0])
+    assert not any(dw[g].any() for g in range(1, E - 1))
