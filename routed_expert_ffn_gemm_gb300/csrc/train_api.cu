@@ -14,13 +14,19 @@ cudaStream_t stream_of(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxRows = 1 << 24;  // as T * k of the layer
 
-long long wait_limit_ns() {
+// How long the waits inside a launch may take, counted from its start: the
+// limit for a launch that gets stuck, and on top of it a long time for what a
+// large one has to do (2 R N K operations at 1e14 a second, the experts'
+// matrices at 5e11 elements; kernels take a tenth of it or less), so that it
+// is not cut off for its size alone.
+long long wait_limit_ns(int R, int N, int K, int E) {
   static long long v = [] {
     const char* s = getenv("MOE_WAIT_LIMIT_NS");
     const long long x = s ? atoll(s) : 0;
     return x > 0 ? x : kDefaultWaitNs;
   }();
-  return v;
+  const double nk = (double)N * K;
+  return v + (long long)(2e-5 * R * nk + 2e-3 * E * nk);
 }
 
 moe_status check_router_losses(int32_t T, int32_t E, int32_t k) {
@@ -66,7 +72,7 @@ moe_status moe_grouped_block_gemm(int32_t R, int32_t K, int32_t N, int32_t E, in
   DeviceCtx ctx;
   MOE_TRY(device_ctx(&ctx));
   BlockGemmArgs a{R,       K,       N,        E,   transposed != 0, out_dtype == MOE_F32, a_codes,        a_scales,
-                  offsets, w_codes, w_scales, out, ctx.num_sms,     ctx.status,           wait_limit_ns()};
+                  offsets, w_codes, w_scales, out, ctx.num_sms,     ctx.status,           wait_limit_ns(R, N, K, E)};
   return block_gemm_launch(a, stream_of(stream));
 }
 
@@ -124,7 +130,7 @@ moe_status moe_grouped_wgrad(int32_t R, int32_t N, int32_t K, int32_t E, int32_t
   DeviceCtx ctx;
   MOE_TRY(device_ctx(&ctx));
   WgradArgs a{R,  N,       K,  E, dy, ld_dy, x, x_scales, offsets, dw, dw_dtype == MOE_F32, accumulate != 0,
-              ctx.num_sms, ctx.status, wait_limit_ns()};
+              ctx.num_sms, ctx.status, wait_limit_ns(R, N, K, E)};
   return grouped_wgrad_launch(a, stream_of(stream));
 }
 

@@ -2,6 +2,9 @@
 time on the current stream: in quick succession, on given streams, from
 several threads, on results past 2^31 elements."""
 
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -13,6 +16,7 @@ from tests.test_gpu_expert_training import close, gemm_case, gen, normal, offset
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -233,3 +237,34 @@ def test_wgrad_past_32_bits():
         n = rows.stop - rows.start
         assert torch.equal(dw[g], api.grouped_wgrad(dy[rows], x[rows], None, offsets_of([n]).to(DEV))[0])
     assert not any(dw[g].any() for g in range(1, E - 1))
+
+
+SHORT_LIMIT = """
+import torch
+from routed_expert_ffn_gemm_gb300 import api
+def codes(*s):
+    return torch.full(s, 0x38, dtype=torch.uint8, device="cuda")  # 1.0
+def ones(*s):
+    return torch.ones(*s, device="cuda")
+for R, E, K, N, t in ((8192, 2, 4096, 14336, False), (8192, 2, 4096, 14336, True), (4096, 64, 4096, 7168, False),
+                      (256, 128, 2048, 7168, False)):
+    off = torch.linspace(0, R, E + 1).to(torch.int32).cuda()
+    w, sw = ((K, N), (K // 128, N // 128)) if t else ((N, K), (N // 128, K // 128))
+    y = api.grouped_block_gemm(codes(R, K), ones(R, K // 128), off, codes(E, *w), ones(E, *sw), t)
+    assert (y == K).all(), (R, E, K, N, t)
+R, E, N, K = 8192, 2, 4096, 14336
+off = torch.tensor([0, 4096, 8192], dtype=torch.int32, device="cuda")
+dy = torch.ones(R, N, dtype=torch.bfloat16, device="cuda")
+dw = api.grouped_wgrad(dy, codes(R, K), ones(R, K // 128), off)
+assert (dw == 4096).all()
+assert api.moe_read_device_status() == api.OK
+print("complete")
+"""
+
+
+def test_long_products_are_not_cut_off():
+    # launches of 0.2 to 1 ms under a limit of 0.05 ms for stuck ones: what
+    # the limit leaves a launch grows with its work
+    r = subprocess.run([sys.executable, "-c", SHORT_LIMIT], cwd=ROOT, env=dict(os.environ, MOE_WAIT_LIMIT_NS="50000"),
+                       capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "complete" in r.stdout, r.stdout + r.stderr

@@ -54,3 +54,12 @@ def test_copies_are_found():
 def test_no_copy_is_multicast(path):
     # the library is also loaded by replicas on several GPUs
     assert not [s for s in statements(path) if "cp.async.bulk" in s and "multicast" in s]
+
+
+def test_wait_limit_grows_with_the_work():
+    # the waits' limit counts from a launch's start: a constant one would end
+    # a product that takes longer than it (600 000 rows of 65 536 x 65 536: 2.2
+    # seconds, 122 GB)
+    text = text_of("train_api.cu")
+    limits = re.findall(r"wait_limit_ns\((.*?)\)", text)
+    assert len(limits) >= 3 and all("R" in a and "N" in a and "K" in a and "E" in a for a in limits)
