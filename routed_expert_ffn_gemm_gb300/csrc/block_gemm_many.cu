@@ -20,8 +20,9 @@
 // ahead: a group's scales at once (460 -> 427 us), the next buffer's barrier
 // polled while this one is added (427 -> 415), two staged store boxes (415 ->
 // 402), the unit's place handed on by warp 2 instead of searched for in front
-// of the stores (12 blocks a unit, 128 experts: 246 -> 234).  Measured: 8192
-// rows of 4 experts 4096 -> 14336 in 398 us, 2.4 PFLOP/s;
+// of the stores (12 blocks a unit, 128 experts: 246 -> 234, graph replays; a
+// call takes 260).  Measured: 8192 rows of 4 experts 4096 -> 14336 in 395 us,
+// 2.4 PFLOP/s;
 // clusters of four with an MMA for each CTA and four buffers took 606, a
 // quarter of the columns a hand-over 590, one issuing warp for both halves 483.
 #include "block_gemm.cuh"

@@ -14,8 +14,12 @@
 // 12 us forward, 6 for the sum over CTAs and 20 for the gradient (a row's
 // loads and reductions, not bandwidth, set that pace: the logits stay in L2),
 // 64 x 8 both directions 9 us.  Sums over tokens
-// go lane -> warp -> CTA -> fixed-order sum over CTAs: no floating-point
-// atomics, so every run gives the same bits.
+// go lane -> warp -> CTA -> fixed-order sum over CTAs without floating-point
+// atomics, and the gradient's kept weights are added in shared memory once for
+// each of a row's distinct experts: every run gives the same bits.
+// Probabilities take __expf: with expf the error against 64 bits is the same
+// (5.0e-8 of the 32768 x 256 gradient's norm, as of the plain form's) and the
+// step takes 45.0 us instead of 43.7.
 #include <math.h>
 
 #include <atomic>

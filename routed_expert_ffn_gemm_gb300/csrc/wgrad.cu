@@ -27,9 +27,9 @@
 // (codes to bf16, zeroed tails), warps 8..15 hold the accumulators.
 //
 // Bound by the tensor cores with many rows an expert (8 experts of 4096 x
-// 14336, 8192 bf16 rows: 605 us, 1.6 PFLOP/s, while the clock holds; 685 in a
-// long run under the power cap), by the conversions when those rows are
-// codes (854 us), by writing dw with few (116 of 128 experts of 1536 x 2048 in
+// 14336, 8192 bf16 rows: 605 us, 1.6 PFLOP/s, while the clock holds; about 700
+// call after call, under the power cap), by the conversions when those rows
+// are codes (875 us), by writing dw with few (116 of 128 experts of 1536 x 2048 in
 // fp32, 16384 rows of codes: 284 us, 6.0 TB/s).
 #include <atomic>
 
