@@ -1,7 +1,8 @@
 /*
  * moe.h -- C ABI of libmoe_gb300.so: the single-GPU forward of one
- * Mixture-of-Experts FFN layer on GB300 (sm_103a), and the operators that
- * train its routed experts in 8 bits (at the end).
+ * Mixture-of-Experts FFN layer on GB300 (sm_103a), and (at the end) the
+ * operators that train its routed experts in 8 bits, run them in 4 bits and
+ * move tokens with gradients.
  *
  * The layer, as the page "MOE推理流程解析" (ffner.com) lays it out:
  *   section 三: the router scores every eligible expert; top-k keeps the
@@ -605,6 +606,155 @@ MOE_API moe_status moe_router_losses_backward(int32_t T, int32_t E, int32_t k, c
                                               float balance_coef, float z_coef, const int32_t *counts,
                                               const float *lse, const float *grad_loss, const float *topk_w,
                                               const float *d_topk_w, float *d_logits, moe_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The experts in 4 bits, and the gradients of the token movement.  No page
+ * counterpart beyond the MXFP4 storage above: the rows that a layer's tokens
+ * become (moe_dispatch, moe_combine_rows), as they are or in MXFP4, products
+ * of MXFP4 rows with MXFP4 weights, and what training needs of the movement.
+ *
+ * MXFP4 rows [rows, cols]: codes [rows, cols/2], two E2M1 codes a byte
+ * (element 2i in the low half of byte i), and scales [rows, cols/32]: byte b
+ * stands for 2^(b - 127), 255 for NaN; a value is E2M1(code) * scale.  MXFP4
+ * weights [E, N, K] have codes [E, N, K/2] and scales [E, K/32, N], as the
+ * layer's MOE_MXFP4 weights.
+ * Assignments whose expert index is negative are dropped: padding tokens, or
+ * an expert's capacity.  They take no row and add nothing; inv_row is -1 there.
+ * Limits: E <= 1024, k <= 32, T * k <= 2^24, rows <= 2^24.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum moe_mx_scale {
+  MOE_MX_FLOOR = 0, /* 2^(floor(log2 a) - 2), the OCP MX rule: the largest
+                       magnitudes of a block, above 6 scales, become 6        */
+  MOE_MX_FIT = 1    /* the least 2^p with a / 2^p <= 6: nothing is clipped    */
+} moe_mx_scale;
+
+/*
+ * moe_dispatch -- tokens to rows grouped by expert.
+ *
+ *   topk_idx  [T, k] int32: expert of each assignment, negative: dropped.
+ *             Values from E on are dropped too and flag MOE_ERR_DEVICE_BOUNDS
+ *   counts    [E] out: assignments of each expert
+ *   offsets   [E+1] out: offsets[e] = sum of counts before e
+ *   row_token [T*k] out: token of each row; -1 from row offsets[E] on
+ *   inv_row   [T, k] out: row of each assignment, or -1
+ *   rows      out, or NULL (maps alone; x is not read then):
+ *             rows_dtype x_dtype: rows[r,:] = x[row_token[r],:], [T*k, d]
+ *             rows_dtype MOE_MXFP4 (d % 32 == 0): codes [T*k, d/2] of them with
+ *             row_scales [T*k, d/32], as moe_quantize_mxfp4 with scale_kind
+ *   x         [T, d] MOE_BF16 or MOE_F32, row pitch ld_x elements
+ * Rows of an expert are in assignment order (bit-exact).  Rows from
+ * offsets[E] on are left as they are.  d % 8 == 0, else MOE_ERR_UNSUPPORTED.
+ * T == 0: counts and offsets are set to zero.
+ *   workspace: moe_dispatch_workspace_size() bytes (the same on every device)
+ */
+MOE_API moe_status moe_dispatch(int32_t T, int32_t d, int32_t E, int32_t k, int32_t x_dtype, int32_t rows_dtype,
+                                int32_t scale_kind, const void *x, int64_t ld_x, const int32_t *topk_idx,
+                                int32_t *counts, int32_t *offsets, int32_t *row_token, int32_t *inv_row,
+                                void *rows, uint8_t *row_scales, void *workspace, size_t workspace_bytes,
+                                moe_stream_t stream);
+MOE_API moe_status moe_dispatch_workspace_size(int32_t T, int32_t E, int32_t k, size_t *bytes);
+
+/*
+ * moe_combine_rows -- rows back to tokens: as moe_combine, with dropped
+ * assignments and, without weights, the gradient of moe_dispatch.
+ *
+ *   out[t,:] = sum_j topk_w[t,j] * rows[inv_row[t,j],:] (+ add[t,:])
+ *
+ * over the assignments with inv_row >= 0, in fp32 in slot order, then add,
+ * rounded once to dtype.
+ *   rows     [R, d] MOE_BF16 or MOE_F32     inv_row [T, k] int32
+ *   topk_w   [T, k] fp32, or NULL: weights of 1 (d_x of moe_dispatch from the
+ *            rows' gradients; add: what reaches x another way)
+ *   add      [T, d] dtype or NULL           out [T, d] dtype (may be add)
+ * inv_row values from R on are skipped and flag MOE_ERR_DEVICE_BOUNDS.
+ * d % 8 == 0, else MOE_ERR_UNSUPPORTED.  T == 0: nothing is enqueued.
+ */
+MOE_API moe_status moe_combine_rows(int32_t T, int32_t d, int32_t k, int32_t R, int32_t dtype, const void *rows,
+                                    const int32_t *inv_row, const float *topk_w, const void *add, void *out,
+                                    moe_stream_t stream);
+
+/*
+ * moe_combine_rows_backward -- the gradients of moe_combine_rows:
+ *
+ *   d_rows[inv_row[t,j],:] = topk_w[t,j] * d_out[t,:]
+ *   d_topk_w[t,j]          = sum_i d_out[t,i] * rows[inv_row[t,j],i]
+ *
+ * (0 where the assignment is dropped; the gradient of add is d_out).  Sums in
+ * fp32 in a fixed order.  d_rows [R, d] dtype out, or NULL; d_topk_w [T, k]
+ * fp32 out, or NULL (rows is not read then).  topk_w NULL: weights of 1.
+ * Rows that no assignment has are left as they are.  inv_row holds each row at
+ * most once.
+ */
+MOE_API moe_status moe_combine_rows_backward(int32_t T, int32_t d, int32_t k, int32_t R, int32_t dtype,
+                                             const void *d_out, const void *rows, const int32_t *inv_row,
+                                             const float *topk_w, void *d_rows, float *d_topk_w,
+                                             moe_stream_t stream);
+
+/*
+ * moe_quantize_mxfp4 -- MXFP4 codes and scales of rows or weights.
+ *
+ *   a     = largest magnitude of the block of 32 columns
+ *   scale = 2^p, p by scale_kind within [-127, 127]; 1 when a == 0
+ *   code  = E2M1(x / 2^p): nearest value, ties to the even code, magnitudes
+ *           above 6 saturated to 6, sign kept
+ * A block with an infinity or a NaN gets scale 255 and codes 0: all of its
+ * values are NaN.  Codes and scales are exact functions of the inputs.
+ *
+ *   x       [rows, cols] MOE_BF16 or MOE_F32, row pitch ld_x elements
+ *   codes   [rows, cols/2] out
+ *   scales  matrix_rows == 0: [rows, cols/32] out; else x is rows/matrix_rows
+ *           weight matrices of matrix_rows rows, scales
+ *           [rows/matrix_rows, cols/32, matrix_rows] out (matrix_rows % 16 == 0)
+ * cols % 32 == 0, else MOE_ERR_UNSUPPORTED.  rows == 0: nothing is enqueued.
+ */
+MOE_API moe_status moe_quantize_mxfp4(int32_t rows, int32_t cols, int32_t x_dtype, int32_t scale_kind,
+                                      int32_t matrix_rows, const void *x, int64_t ld_x, uint8_t *codes,
+                                      uint8_t *scales, moe_stream_t stream);
+
+/*
+ * moe_mxfp4_values -- the values that MXFP4 codes stand for, rounded to dtype
+ * (exact but where it over- or underflows); sizes and layouts as
+ * moe_quantize_mxfp4.   out [rows, cols] MOE_BF16 or MOE_F32
+ */
+MOE_API moe_status moe_mxfp4_values(int32_t rows, int32_t cols, int32_t dtype, int32_t matrix_rows,
+                                    const uint8_t *codes, const uint8_t *scales, void *out, moe_stream_t stream);
+
+/*
+ * moe_swiglu_mxfp4 -- h = SiLU(g) * u in fp32 as MXFP4 rows.
+ *
+ *   g, u     [R, ffn] bf16, row pitch ld elements each (the halves of one
+ *            [R, 2 ffn] product: u = g + ffn, ld = 2 ffn)
+ *   codes    [R, ffn/2] out      scales [R, ffn/32] out
+ *   h        [R, ffn] bf16 out, or NULL
+ * ffn % 32 == 0, else MOE_ERR_UNSUPPORTED.  R == 0: nothing is enqueued.
+ */
+MOE_API moe_status moe_swiglu_mxfp4(int32_t R, int32_t ffn, int32_t scale_kind, const void *g, const void *u,
+                                    int64_t ld, uint8_t *codes, uint8_t *scales, void *h, moe_stream_t stream);
+
+/*
+ * moe_grouped_mxfp4_gemm -- MXFP4 rows times MXFP4 weights.  For every row r
+ * of expert e (offsets [E+1] int32 on the device):
+ *
+ *   out[r,n] = sum_b 2^(sa[r,b] - 127) * 2^(sw[e,b,n] - 127) *
+ *              sum_{i in block b} a[r,i] * w[e,n,i]
+ *
+ * products exact, sums in fp32 on the tensor cores, rounded once to out_dtype.
+ *   a_codes [R, K/2]      a_scales [R, K/32]
+ *   w_codes [E, N, K/2]   w_scales [E, K/32, N]
+ *   out     [R, N] MOE_BF16 or MOE_F32, row pitch ld_out elements
+ * A scale of 255 makes every result that it enters NaN.  The gradient of the
+ * rows is the same product with the weights quantised along N (the codes of
+ * each matrix's transpose).  Offsets outside [0, R], or decreasing ones, are
+ * clamped and flag MOE_ERR_DEVICE_BOUNDS.  Rows outside every expert's range
+ * are left untouched.  K % 32 == 0 and N % 16 == 0, else MOE_ERR_UNSUPPORTED;
+ * R == 0: nothing is enqueued.
+ */
+MOE_API moe_status moe_grouped_mxfp4_gemm(int32_t R, int32_t K, int32_t N, int32_t E, int32_t out_dtype,
+                                          const uint8_t *a_codes, const uint8_t *a_scales, const int32_t *offsets,
+                                          const uint8_t *w_codes, const uint8_t *w_scales, void *out,
+                                          int64_t ld_out, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

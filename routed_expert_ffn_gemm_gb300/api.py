@@ -84,6 +84,14 @@ _SIGS = {
     "moe_router_losses_workspace_size": [_I, _I, ctypes.POINTER(ctypes.c_size_t)],
     "moe_router_losses_workspace_size_for": [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)],
     "moe_router_losses_backward": [_I] * 3 + [_VP] * 3 + [_F, _F] + [_VP] * 7,
+    "moe_dispatch": [_I] * 7 + [_VP, _L] + [_VP] * 8 + [ctypes.c_size_t, _VP],
+    "moe_dispatch_workspace_size": [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_combine_rows": [_I] * 5 + [_VP] * 6,
+    "moe_combine_rows_backward": [_I] * 5 + [_VP] * 7,
+    "moe_quantize_mxfp4": [_I] * 5 + [_VP, _L] + [_VP] * 3,
+    "moe_mxfp4_values": [_I] * 4 + [_VP] * 4,
+    "moe_swiglu_mxfp4": [_I] * 3 + [_VP, _VP, _L] + [_VP] * 4,
+    "moe_grouped_mxfp4_gemm": [_I] * 5 + [_VP] * 6 + [_L, _VP],
 }
 STAGES = ("router", "permute", "gate_up", "down", "shared", "combine")
 EXPORTS = tuple(_SIGS)
@@ -701,3 +709,265 @@ def router_losses_backward(logits, topk_idx, losses: RouterLosses, grad=None, to
           _ptr(losses.counts), _ptr(losses.lse), _ptr(grad), _ptr(topk_w), _ptr(d_topk_w), _ptr(d_logits),
           _stream(None))
     return d_logits
+
+
+# ---------------------------------------------------------------------------
+# the experts in 4 bits, and the gradients of the token movement
+# ---------------------------------------------------------------------------
+
+MX_BLOCK = 32
+MX_SCALE = {"floor": 0, "fit": 1}
+
+
+def _mx_scale(kind) -> int:
+    if kind not in MX_SCALE:
+        raise ValueError(f"scale: {kind!r}, the call takes {sorted(MX_SCALE)}")
+    return MX_SCALE[kind]
+
+
+def _here(*tensors) -> None:
+    """The tensors are on the current device: the kernels run there."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor on {t.device}, the current device is cuda:{dev}")
+
+
+class Dispatched(NamedTuple):
+    """What dispatch returns: the rows [T * k, d] (codes [T * k, d / 2] with
+    scales [T * k, d / 32] where quantised), offsets [E + 1], counts [E],
+    row_token [T * k] and inv_row [T, k]."""
+    rows: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    offsets: torch.Tensor
+    counts: torch.Tensor
+    row_token: torch.Tensor
+    inv_row: torch.Tensor
+
+
+class CombineGrads(NamedTuple):
+    """What combine_backward returns: the gradients of the rows and of the
+    routing weights, None where not asked for."""
+    dy: Optional[torch.Tensor]
+    dw: Optional[torch.Tensor]
+
+
+class MxSwiglu(NamedTuple):
+    """What swiglu_mxfp4 returns: h as codes [R, ffn / 2] and scales [R, ffn /
+    32], and in bf16 where asked for."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    h: Optional[torch.Tensor]
+
+
+@functools.lru_cache(maxsize=256)
+def moe_dispatch_workspace_size(T: int, E: int, k: int) -> int:
+    n = ctypes.c_size_t(0)
+    _call("moe_dispatch_workspace_size", T, E, k, ctypes.byref(n))
+    return int(n.value)
+
+
+def _slots(idx, name) -> tuple:
+    if idx.dim() != 2 or idx.dtype is not torch.int32:
+        raise ValueError(f"{name}: {idx.dtype} {list(idx.shape)}, the call takes torch.int32 [T, k]")
+    return tuple(idx.shape)
+
+
+def dispatch(x, topk_idx, E, quantize=None, rows=None, scales=None, workspace=None, stream=None) -> Dispatched:
+    """moe_dispatch of x [T, d] (its rows may lie apart) by topk_idx [T, k],
+    negative where an assignment is dropped: rows of x's type, or MXFP4 with
+    quantize "floor" or "fit".  x None: the maps alone."""
+    if stream is not None:
+        return _on_stream(stream, dispatch, x, topk_idx, E, quantize, rows, scales, workspace)
+    T, k = _slots(topk_idx, "topk_idx")
+    _here(x, topk_idx, rows, scales, workspace)
+    R, dev, empty = T * k, topk_idx.device, torch.empty
+    d, ld, kind, out_kind, mx = 8, 8, DTYPE["bf16"], DTYPE["bf16"], 0
+    if x is None:
+        if quantize is not None or rows is not None or scales is not None:
+            raise ValueError("rows: there are none without x")
+    else:
+        ld = _rows(x, "x")
+        kind = out_kind = _type(x.dtype, "x")
+        d = x.shape[1]
+        if x.shape[0] != T:
+            raise ValueError(f"x: {list(x.shape)}, topk_idx has {T} tokens")
+        if quantize is None:
+            shape, t = (R, d), x.dtype
+            if scales is not None:
+                raise ValueError("scales: there are none without quantize")
+        else:
+            mx, out_kind = _mx_scale(quantize), DTYPE["mxfp4"]
+            if d % MX_BLOCK:
+                raise ValueError(f"x: {d} columns are no multiple of {MX_BLOCK}")
+            shape, t = (R, d // 2), torch.uint8
+            if scales is None:
+                scales = empty((R, d // MX_BLOCK), dtype=torch.uint8, device=dev)
+            else:
+                _exact(scales, "scales", (R, d // MX_BLOCK), torch.uint8)
+        if rows is None:
+            rows = empty(shape, dtype=t, device=dev)
+        else:
+            _exact(rows, "rows", shape, t)
+    offsets = empty(E + 1, dtype=torch.int32, device=dev)
+    counts = empty(E, dtype=torch.int32, device=dev)
+    row_token = empty(R, dtype=torch.int32, device=dev)
+    inv_row = empty((T, k), dtype=torch.int32, device=dev)
+    if workspace is None:
+        n = moe_dispatch_workspace_size(T, E, k)
+        workspace = empty(n, dtype=torch.uint8, device=dev) if n else None
+    _call("moe_dispatch", T, d, E, k, kind, out_kind, mx, None if x is None else _pitched(x), ld, _ptr(topk_idx),
+          _ptr(counts), _ptr(offsets), _ptr(row_token), _ptr(inv_row), _ptr(rows), _ptr(scales), _ptr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(None))
+    return Dispatched(rows, scales, offsets, counts, row_token, inv_row)
+
+
+def combine(y, inv_row, topk_w=None, add=None, out=None, stream=None):
+    """moe_combine_rows: rows y [R, d] weighted (topk_w None: ones), summed
+    back to tokens and added to add [T, d] -> [T, d]."""
+    if stream is not None:
+        return _on_stream(stream, combine, y, inv_row, topk_w, add, out)
+    T, k = _slots(inv_row, "inv_row")
+    if y.dim() != 2:
+        raise ValueError("y: [R, d] is expected")
+    _here(y, inv_row, topk_w, add, out)
+    (R, d), kind = y.shape, _type(y.dtype, "y")
+    _exact(topk_w, "topk_w", (T, k), torch.float32)
+    _exact(add, "add", (T, d), y.dtype)
+    if out is None:
+        out = torch.empty((T, d), dtype=y.dtype, device=y.device)
+    else:
+        _exact(out, "out", (T, d), y.dtype)
+    _call("moe_combine_rows", T, d, k, R, kind, _ptr(y), _ptr(inv_row), _ptr(topk_w), _ptr(add), _ptr(out), _stream(None))
+    return out
+
+
+def dispatch_backward(d_rows, inv_row, add=None, out=None, stream=None):
+    """The gradient of dispatch's x from its rows' d_rows [R, d], added to add
+    [T, d] (what reaches x another way)."""
+    return combine(d_rows, inv_row, None, add, out, stream)
+
+
+def combine_backward(d_out, y, inv_row, topk_w=None, want_dy=True, want_dw=True, dy=None, stream=None) -> CombineGrads:
+    """moe_combine_rows_backward: the gradients of combine's y and topk_w from
+    d_out [T, d].  Rows that no assignment has stay as they are in dy."""
+    if stream is not None:
+        return _on_stream(stream, combine_backward, d_out, y, inv_row, topk_w, want_dy, want_dw, dy)
+    T, k = _slots(inv_row, "inv_row")
+    if y.dim() != 2:
+        raise ValueError("y: [R, d] is expected")
+    _here(d_out, y, inv_row, topk_w, dy)
+    (R, d), kind = y.shape, _type(y.dtype, "y")
+    _exact(d_out, "d_out", (T, d), y.dtype)
+    _exact(topk_w, "topk_w", (T, k), torch.float32)
+    if dy is not None:
+        _exact(dy, "dy", (R, d), y.dtype)
+    elif want_dy:
+        dy = torch.empty((R, d), dtype=y.dtype, device=y.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=y.device) if want_dw else None
+    _call("moe_combine_rows_backward", T, d, k, R, kind, _ptr(d_out), _ptr(y), _ptr(inv_row), _ptr(topk_w), _ptr(dy),
+          _ptr(dw), _stream(None))
+    return CombineGrads(dy, dw)
+
+
+def _mx_shapes(shape, weights: bool) -> tuple:
+    """Rows, rows of a weight matrix (0: none) and the shapes of codes and
+    scales of values of this shape."""
+    if weights and len(shape) != 3:
+        raise ValueError(f"weights: {list(shape)}, the call takes [E, N, K]")
+    cols = shape[-1]
+    if cols % MX_BLOCK:
+        raise ValueError(f"{cols} columns are no multiple of {MX_BLOCK}")
+    rows, blocks = 1, cols // MX_BLOCK
+    for n in shape[:-1]:
+        rows *= n
+    codes = (*shape[:-1], cols // 2)
+    return (rows, shape[1], codes, (shape[0], blocks, shape[1])) if weights else (rows, 0, codes, (*shape[:-1], blocks))
+
+
+def quantize_mxfp4(x, scale="floor", weights=False, codes=None, scales=None, stream=None):
+    """moe_quantize_mxfp4 of x [..., cols] (a matrix's rows may lie apart):
+    (codes uint8 [..., cols / 2], scales uint8 [..., cols / 32]); with weights
+    of x [E, N, K], scales [E, K / 32, N] as the products take them."""
+    if stream is not None:
+        return _on_stream(stream, quantize_mxfp4, x, scale, weights, codes, scales)
+    mx, kind = _mx_scale(scale), _type(x.dtype, "x")
+    rows, matrix, cshape, sshape = _mx_shapes(x.shape, weights)
+    _here(x, codes, scales)
+    m = x if x.dim() == 2 else x.reshape(rows, x.shape[-1])
+    ld = _rows(m, "x")
+    if codes is None:
+        codes = torch.empty(cshape, dtype=torch.uint8, device=x.device)
+    else:
+        _exact(codes, "codes", cshape, torch.uint8)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.uint8, device=x.device)
+    else:
+        _exact(scales, "scales", sshape, torch.uint8)
+    _call("moe_quantize_mxfp4", rows, m.shape[1], kind, mx, matrix, _pitched(m), ld, _ptr(codes), _ptr(scales), _stream(None))
+    return codes, scales
+
+
+def mxfp4_values(codes, scales, dtype=torch.bfloat16, weights=False, out=None, stream=None):
+    """moe_mxfp4_values: what quantize_mxfp4's codes and scales stand for."""
+    if stream is not None:
+        return _on_stream(stream, mxfp4_values, codes, scales, dtype, weights, out)
+    shape = (*codes.shape[:-1], 2 * codes.shape[-1])
+    rows, matrix, cshape, sshape = _mx_shapes(shape, weights)
+    _here(codes, scales, out)
+    kind = _type(dtype if out is None else out.dtype, "out")
+    _exact(codes, "codes", cshape, torch.uint8)
+    _exact(scales, "scales", sshape, torch.uint8)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=codes.device)
+    else:
+        _exact(out, "out", shape, out.dtype)
+    _call("moe_mxfp4_values", rows, shape[-1], kind, matrix, _ptr(codes), _ptr(scales), _ptr(out), _stream(None))
+    return out
+
+
+def swiglu_mxfp4(g, u, scale="floor", want_h=False, stream=None) -> MxSwiglu:
+    """moe_swiglu_mxfp4 of g and u [R, ffn] bf16 (for instance the halves of
+    one product's rows)."""
+    if stream is not None:
+        return _on_stream(stream, swiglu_mxfp4, g, u, scale, want_h)
+    mx, ld = _mx_scale(scale), _rows(g, "g", torch.bfloat16)
+    if _rows(u, "u", torch.bfloat16) != ld or u.shape != g.shape:
+        raise ValueError("g and u: two matrices of one shape and row pitch are expected")
+    _here(g, u)
+    (R, f), dev = g.shape, g.device
+    if f % MX_BLOCK:
+        raise ValueError(f"g: {f} columns are no multiple of {MX_BLOCK}")
+    codes = torch.empty((R, f // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((R, f // MX_BLOCK), dtype=torch.uint8, device=dev)
+    h = torch.empty((R, f), dtype=torch.bfloat16, device=dev) if want_h else None
+    _call("moe_swiglu_mxfp4", R, f, mx, _pitched(g), _pitched(u), ld, _ptr(codes), _ptr(scales), _ptr(h), _stream(None))
+    return MxSwiglu(codes, scales, h)
+
+
+def grouped_mxfp4_gemm(a, a_scales, offsets, w, w_scales, out_dtype=torch.bfloat16, out=None, stream=None):
+    """moe_grouped_mxfp4_gemm: MXFP4 rows a [R, K / 2] with scales [R, K / 32]
+    of each expert times its w [E, N, K / 2] with scales [E, K / 32, N] -> [R,
+    N] (out's rows may lie apart)."""
+    if stream is not None:
+        return _on_stream(stream, grouped_mxfp4_gemm, a, a_scales, offsets, w, w_scales, out_dtype, out)
+    if a.dim() != 2 or w.dim() != 3 or a.shape[1] != w.shape[2]:
+        raise ValueError(f"a: {list(a.shape)} and w: {list(w.shape)}, the call takes [R, K / 2] and [E, N, K / 2]")
+    _here(a, a_scales, offsets, w, w_scales, out)
+    (R, half), (E, N, _) = a.shape, w.shape
+    K = 2 * half
+    if K % MX_BLOCK:
+        raise ValueError(f"a: {K} columns are no multiple of {MX_BLOCK}")
+    kind = _type(out_dtype if out is None else out.dtype, "out")
+    _exact(a, "a", (R, half), torch.uint8)
+    _exact(a_scales, "a_scales", (R, K // MX_BLOCK), torch.uint8)
+    _exact(offsets, "offsets", (E + 1,), torch.int32)
+    _exact(w, "w", (E, N, half), torch.uint8)
+    _exact(w_scales, "w_scales", (E, K // MX_BLOCK, N), torch.uint8)
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype, device=a.device)
+    elif out.shape != (R, N):
+        raise ValueError(f"out: {list(out.shape)}, the call takes {[R, N]}")
+    _call("moe_grouped_mxfp4_gemm", R, K, N, E, kind, _ptr(a), _ptr(a_scales), _ptr(offsets), _ptr(w), _ptr(w_scales),
+          _pitched(out), _rows(out, "out"), _stream(None))
+    return out

@@ -93,22 +93,6 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_blocks_kernel(const void
   }
 }
 
-// sigmoid(g) within a few units of 2^-23, 0 where exp(-g) overflows.
-// exp(-g) = 2^-(g hi) (1 - g lo ln 2) with log2 e = hi + lo: hi has 16 bits,
-// so that g hi is exact for the 8 bits of a bf16 gate and the 4 of a kept one
-// (rounded, with log2 e's own rounding, 4 units at g = -10 and 28 at -60), and
-// the rest is linear (its square is below 2^-23 where exp(-g) is finite).  32768 x
-// 2048 forward and backward: 105 and 144 us, 103 and 142 with __expf, 110 and
-// 147 with expf.
-__device__ __forceinline__ float sigmoid(float g) {
-  constexpr float kHi = 47274.f / 32768.f, kLoLn2 = 4.888495e-6f;
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -kHi));
-  e *= fmaxf(fmaf(g, -kLoLn2, 1.f), 0.f);
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return r;
-}
-
 __global__ void __launch_bounds__(kThreads, 4) swiglu_save_kernel(const SwigluSaveArgs a, uint32_t tasks, uint32_t nb) {
   griddep_begin();
   const uint32_t step = gridDim.x * kGroups, f = (uint32_t)a.f;

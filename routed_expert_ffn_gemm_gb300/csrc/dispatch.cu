@@ -1,0 +1,314 @@
+// Dispatch: tokens to rows grouped by expert, dropped assignments without a
+// row, rows as they are or as MXFP4.
+//
+// A row's place is its expert's offset plus the number of earlier assignments
+// to the same expert: counts of 32 assignments at a time by match_any, prefix
+// sums over warps, chunks and experts, no atomics whose order shows.
+//
+//   few assignments (kSmallRows): one launch.  Every CTA works the maps out for
+//     itself in shared memory (they are a few KB) and then moves its share of
+//     the rows; CTA 0 writes the maps.
+//   many: counts of each chunk; prefix sums over the chunks, a CTA for each 32
+//     experts; then a CTA a chunk ranks its assignments and moves its tokens.
+//
+// A token is read once and written to its k rows, so that x comes from memory
+// once; as MXFP4 it is quantised once.  Memory bounds the large calls, launch
+// and the chain of prefix sums the small ones.
+#include "mxfp4.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kSmallRows = 2048;
+constexpr int kSmallThreads = 512;
+constexpr int kChunkRows = 256;  // assignments of a chunk at most (whole tokens)
+constexpr int kThreads = 256;
+
+enum Move { kNone, kCopy, kMxBf16, kMxF32 };
+
+// Assignments of a chunk: whole tokens, kChunkRows at most.
+__host__ __device__ inline int chunk_of(int k) { return kChunkRows / k * k; }
+
+__device__ __forceinline__ uint32_t lanes_below() {
+  uint32_t m;
+  asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
+  return m;
+}
+
+// The expert of assignment a, -1 where it takes no row.
+__device__ __forceinline__ int expert_of(const DispatchArgs& p, int a) {
+  const int e = p.idx[a];
+  if (e < p.E) return e < 0 ? -1 : e;
+  set_device_status(p.status, MOE_ERR_DEVICE_BOUNDS);
+  return -1;
+}
+
+// Rank of the lane's assignment among the warp's earlier ones of its expert;
+// cnt[E] of the warp counts them.
+__device__ __forceinline__ int rank_in_warp(int e, int* cnt) {
+  const uint32_t peers = __match_any_sync(0xffffffffu, e);
+  const int before = e >= 0 ? cnt[e] : 0;
+  __syncwarp();
+  if (e >= 0 && (peers & lanes_below()) == 0u) cnt[e] = before + __popc(peers);
+  __syncwarp();
+  return before + __popc(peers & lanes_below());
+}
+
+// Exclusive prefix sums of tot[0..E) into base[0..E], by the whole CTA
+// (THREADS threads, E <= 1024); tot and base may be the same.
+template <int THREADS>
+__device__ __forceinline__ void expert_bases(const int* tot, int* base, int E, int* warp_tot) {
+  constexpr int EACH = 1024 / THREADS;  // consecutive experts of a thread
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v[EACH], sum = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = threadIdx.x * EACH + i;
+    v[i] = e < E ? tot[e] : 0;
+    sum += v[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  int run = incl - sum;
+  for (int w = 0; w < warp; ++w) run += warp_tot[w];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = threadIdx.x * EACH + i;
+    if (e <= E) base[e] = run;
+    run += v[i];
+  }
+  if (E == 1024 && threadIdx.x == THREADS - 1) base[E] = run;
+  __syncthreads();
+}
+
+// Pieces of a token's row that a warp moves at a time: 32 lanes of 16 bytes
+// (kCopy) or of a block of 32 columns.
+template <Move M>
+__device__ __forceinline__ int pieces_of(const DispatchArgs& p) {
+  return M == kCopy ? (p.d * (p.f32 ? 4 : 2) / 16 + 31) / 32 : (p.d / kMxBlock + 31) / 32;
+}
+
+// One warp: piece `c` of token t to the rows in `rows` (k of them, -1: none).
+template <Move M, bool WIDE>
+__device__ __forceinline__ void move_piece(const DispatchArgs& p, int t, int c, const int* rows) {
+  const int at = c * 32 + (threadIdx.x & 31);
+  if constexpr (M == kCopy) {
+    const int vecs = p.d * (p.f32 ? 4 : 2) / 16;
+    if (at >= vecs) return;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) +
+                                                         (size_t)t * p.ldx * (p.f32 ? 4 : 2)) + at);
+    for (int j = 0; j < p.k; ++j)
+      if (rows[j] >= 0) static_cast<uint4*>(p.rows)[(size_t)rows[j] * vecs + at] = v;
+  } else {
+    constexpr bool F32 = M == kMxF32;
+    const int nb = p.d / kMxBlock;
+    if (at >= nb) return;
+    MxBlock<F32> b;
+    load_words<MxBlock<F32>::WORDS, WIDE>(
+        static_cast<const uint8_t*>(p.x) + ((size_t)t * p.ldx + (size_t)at * kMxBlock) * (F32 ? 4 : 2), b.w);
+    uint4 codes;
+    const uint32_t s = b.codes(p.fit, codes);
+    for (int j = 0; j < p.k; ++j)
+      if (rows[j] >= 0) {
+        const size_t to = (size_t)rows[j] * nb + at;
+        static_cast<uint4*>(p.rows)[to] = codes;
+        p.row_scales[to] = (uint8_t)s;
+      }
+  }
+}
+
+// ------------------------------------------------------------ few assignments
+// smem: cnt[16][E], base[E + 1], row_of[R]
+template <Move M, bool WIDE>
+__global__ void __launch_bounds__(kSmallThreads) dispatch_small_kernel(const DispatchArgs p) {
+  griddep_begin();
+  constexpr int WARPS = kSmallThreads / 32;
+  extern __shared__ int sm[];
+  __shared__ int warp_tot[WARPS];
+  const int R = p.T * p.k, E = p.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* cnt = sm;
+  int* base = cnt + WARPS * E;
+  int* row_of = base + E + 1;
+  for (int i = threadIdx.x; i < WARPS * E; i += kSmallThreads) cnt[i] = 0;
+  __syncthreads();
+  // a warp's assignments are consecutive, so that warps are in order; the rank
+  // and the expert of each wait packed in row_of (R <= 2^11, E <= 2^10)
+  const int seg = (R + WARPS * 32 - 1) / (WARPS * 32) * 32, a0 = min(R, warp * seg), a1 = min(R, a0 + seg);
+  for (int s = a0; s < a1; s += 32) {
+    const int a = s + lane, e = a < a1 ? expert_of(p, a) : -1;
+    const int rank = rank_in_warp(e, cnt + warp * E);
+    if (a < a1) row_of[a] = e < 0 ? -1 : e << 16 | rank;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kSmallThreads) {
+    int run = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      const int c = cnt[w * E + e];
+      cnt[w * E + e] = run;
+      run += c;
+    }
+    base[e] = run;
+  }
+  __syncthreads();
+  const bool maps = blockIdx.x == 0;
+  if (maps)
+    for (int e = threadIdx.x; e < E; e += kSmallThreads) p.counts[e] = base[e];
+  expert_bases<kSmallThreads>(base, base, E, warp_tot);
+  for (int a = threadIdx.x; a < R; a += kSmallThreads) {
+    const int v = row_of[a], e = v >> 16;
+    const int row = v < 0 ? -1 : base[e] + cnt[a / seg * E + e] + (v & 0xffff);
+    row_of[a] = row;
+    if (maps) {
+      p.inv_row[a] = row;
+      if (row >= 0) p.row_token[row] = a / p.k;
+    }
+  }
+  if (maps) {
+    for (int e = threadIdx.x; e <= E; e += kSmallThreads) p.offsets[e] = base[e];
+    for (int r = base[E] + threadIdx.x; r < R; r += kSmallThreads) p.row_token[r] = -1;
+  }
+  if constexpr (M != kNone) {
+    __syncthreads();
+    const int pieces = pieces_of<M>(p);
+    // (the pieces go to the CTAs first, then to their warps)
+    for (long long i = blockIdx.x + (long long)gridDim.x * warp; i < (long long)p.T * pieces;
+         i += (long long)gridDim.x * WARPS) {
+      const int t = (int)(i / pieces);
+      move_piece<M, WIDE>(p, t, (int)(i - (long long)t * pieces), row_of + t * p.k);
+    }
+  }
+}
+
+// ----------------------------------------------------------- many assignments
+// chunks[c][e]: assignments of chunk c to expert e
+__global__ void __launch_bounds__(kThreads) dispatch_count_kernel(const DispatchArgs p, int chunk) {
+  griddep_begin();
+  extern __shared__ int sm[];
+  for (int e = threadIdx.x; e < p.E; e += kThreads) sm[e] = 0;
+  __syncthreads();
+  const long long a = (long long)blockIdx.x * chunk + threadIdx.x;
+  if ((int)threadIdx.x < chunk && a < (long long)p.T * p.k) {
+    const int e = expert_of(p, (int)a);
+    if (e >= 0) atomicAdd(&sm[e], 1);  // (a count: the order does not show)
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kThreads) p.chunks[(size_t)blockIdx.x * p.E + e] = sm[e];
+}
+
+// Each chunk's counts become the sums over the chunks before it; counts[e] the
+// total.  A CTA takes 32 experts (the lanes), a warp a slice of the chunks.
+__global__ void __launch_bounds__(1024) dispatch_scan_kernel(int n_chunks, int E, int32_t* __restrict__ chunks,
+                                                             int32_t* __restrict__ counts) {
+  griddep_begin();
+  __shared__ int part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  const int per = (n_chunks + 31) / 32, c0 = min(n_chunks, warp * per), c1 = min(n_chunks, c0 + per);
+  int sum = 0;
+  if (e < E)
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) sum += chunks[(size_t)c * E + e];
+  part[warp][lane] = sum;
+  __syncthreads();
+  int run = 0;
+  for (int w = 0; w < warp; ++w) run += part[w][lane];
+  if (e >= E) return;
+  if (warp == 31) counts[e] = run + sum;
+#pragma unroll 8
+  for (int c = c0; c < c1; ++c) {
+    const int v = chunks[(size_t)c * E + e];
+    chunks[(size_t)c * E + e] = run;
+    run += v;
+  }
+}
+
+// smem: cnt[8][E], base[E + 1], row_of[kChunkRows]
+template <Move M, bool WIDE>
+__global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchArgs p, int chunk) {
+  griddep_begin();
+  constexpr int WARPS = kThreads / 32;
+  extern __shared__ int sm[];
+  __shared__ int warp_tot[WARPS];
+  const int R = p.T * p.k, E = p.E, warp = threadIdx.x >> 5;
+  int* cnt = sm;
+  int* base = cnt + WARPS * E;
+  int* row_of = base + E + 1;
+  for (int i = threadIdx.x; i < WARPS * E; i += kThreads) cnt[i] = 0;
+  __syncthreads();
+  const int first = blockIdx.x * chunk, n = min(chunk, R - first);
+  const int a = first + threadIdx.x;
+  const int e = (int)threadIdx.x < n ? expert_of(p, a) : -1;
+  const int rank = rank_in_warp(e, cnt + warp * E);
+  expert_bases<kThreads>(p.counts, base, E, warp_tot);
+  for (int x = threadIdx.x; x < E; x += kThreads) {
+    int run = base[x] + p.chunks[(size_t)blockIdx.x * E + x];
+    for (int w = 0; w < WARPS; ++w) {
+      const int c = cnt[w * E + x];
+      cnt[w * E + x] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    const int row = e < 0 ? -1 : cnt[warp * E + e] + rank;
+    row_of[threadIdx.x] = row;
+    p.inv_row[a] = row;
+    if (row >= 0) p.row_token[row] = a / p.k;
+    if (a >= base[E]) p.row_token[a] = -1;
+  }
+  if (blockIdx.x == 0)
+    for (int x = threadIdx.x; x <= E; x += kThreads) p.offsets[x] = base[x];
+  if constexpr (M != kNone) {
+    __syncthreads();
+    const int pieces = pieces_of<M>(p), tokens = n / p.k, t0 = first / p.k;
+    for (int t = warp; t < tokens; t += WARPS)
+#pragma unroll 4
+      for (int c = 0; c < pieces; ++c) move_piece<M, WIDE>(p, t0 + t, c, row_of + t * p.k);
+  }
+}
+
+template <Move M, bool WIDE>
+moe_status launch(const DispatchArgs& a, cudaStream_t s) {
+  const int R = a.T * a.k;
+  if (R <= kSmallRows) {
+    constexpr int WARPS = kSmallThreads / 32;
+    const size_t smem = sizeof(int) * ((size_t)WARPS * a.E + a.E + 1 + R);
+    if (smem > 48 * 1024)
+      MOE_TRY_CUDA(cudaFuncSetAttribute(dispatch_small_kernel<M, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)(sizeof(int) * ((size_t)WARPS * 1024 + 1025 + kSmallRows))));
+    const int per = M == kNone ? 0 : M == kCopy ? (a.d * (a.f32 ? 4 : 2) / 16 + 31) / 32 : (a.d / kMxBlock + 31) / 32;
+    const long long pieces = (long long)a.T * per;
+    const int grid = M == kNone ? 1 : (int)(pieces < a.num_sms ? pieces : a.num_sms);
+    MOE_TRY_CUDA(launch_k(dispatch_small_kernel<M, WIDE>, dim3(grid), dim3(kSmallThreads), smem, s, a));
+    return MOE_OK;
+  }
+  const int chunk = chunk_of(a.k), n = ceil_div(R, chunk);
+  MOE_TRY_CUDA(launch_k(dispatch_count_kernel, dim3(n), dim3(kThreads), sizeof(int) * a.E, s, a, chunk));
+  MOE_TRY_CUDA(launch_k(dispatch_scan_kernel, dim3(ceil_div(a.E, 32)), dim3(1024), 0, s, n, a.E, a.chunks, a.counts));
+  const size_t smem = sizeof(int) * ((size_t)(kThreads / 32) * a.E + a.E + 1 + kChunkRows);
+  MOE_TRY_CUDA(launch_k(dispatch_move_kernel<M, WIDE>, dim3(n), dim3(kThreads), smem, s, a, chunk));
+  return MOE_OK;
+}
+
+}  // namespace
+
+// Counts of each chunk (nothing with few assignments).
+size_t dispatch_workspace(int T, int E, int k) {
+  const int R = T * k;
+  return R <= kSmallRows ? 0 : (size_t)ceil_div(R, chunk_of(k)) * E * sizeof(int32_t);
+}
+
+moe_status dispatch_launch(const DispatchArgs& a, cudaStream_t s) {
+  if (a.rows == nullptr) return launch<kNone, false>(a, s);
+  if (!a.to_mx) return launch<kCopy, false>(a, s);
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * (a.f32 ? 4 : 2))) & 31u) == 0;
+  if (a.f32) return wide ? launch<kMxF32, true>(a, s) : launch<kMxF32, false>(a, s);
+  return wide ? launch<kMxBf16, true>(a, s) : launch<kMxBf16, false>(a, s);
+}
+
+}  // namespace moe

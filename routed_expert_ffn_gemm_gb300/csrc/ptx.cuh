@@ -441,6 +441,55 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::mxf4: E2M1 codes, two a byte, 64 of
+// the reduction per instruction, with a power of two for each 32 of a row of A
+// and of B in tensor memory; issued as the forms above.  M x N 128 x N (ONE CTA)
+// or 256 x N (PAIR: each CTA holds its own 128 rows' scales of A and all of B's).
+template <bool PAIR>
+__device__ __forceinline__ void mma_mxf4_one(uint32_t one, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t a_scale, uint32_t b_scale, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%6], [%7], p;\n\t}\n" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(one), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%6], [%7], p;\n\t}\n" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(one), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+        : "memory");
+}
+
+// 512 bytes of shared memory (32 rows of 16 bytes) to four columns of tensor
+// memory, the same for each 32 lanes: the scales of 128 rows, row m's four
+// consecutive scale bytes at 16 (m % 32) + 4 (m / 32).  In order with the MMAs
+// of the same thread.  PAIR: in both CTAs, each from its own shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_cp_scales_one(uint32_t one, uint32_t taddr, uint64_t desc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr),
+        "l"(desc), "r"(one)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr),
+        "l"(desc), "r"(one)
+        : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16: A read from tensor memory
 // (row m of A in lane m, two 16-bit elements per 32-bit column, K along
 // the columns).
@@ -607,6 +656,15 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw64(uint32_t smem_addr, uint32_t m
   d |= (uint64_t)4 << 61;  // swizzle 64B
   return d;
 }
+// The same of rows of 16 bytes without swizzling, 8-row groups 128 bytes apart:
+// what tmem_cp_scales_one reads.
+__device__ __forceinline__ uint64_t sdesc_rows16(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
 // Instruction descriptor bits of MN-major operands.
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
@@ -625,6 +683,20 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4)                           // D format: f32
          | ((uint32_t)(N >> 3) << 17)        // N >> 3
          | ((uint32_t)(M >> 4) << 24);       // M >> 4
+}
+
+// Instruction descriptor of the block-scaled kinds (PTX ISA, tcgen05 instruction
+// descriptor of kind::mxf4), E2M1 A and B, UE8M0 scales, fp32 D, shape M x N.
+// `half`: which two of a scale word's four bytes the 64 of the reduction take
+// (0: bytes 0 and 1, 1: bytes 2 and 3).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
+  return ((uint32_t)(2 * half) << 4)         // B scale data id
+         | (1u << 7)                         // A format: E2M1
+         | (1u << 10)                        // B format: E2M1
+         | ((uint32_t)(N >> 3) << 17)        // N >> 3
+         | (1u << 23)                        // scale format: UE8M0
+         | ((uint32_t)(M >> 7) << 27)        // M >> 7
+         | ((uint32_t)(2 * half) << 29);     // A scale data id
 }
 
 }  // namespace ptx

@@ -158,6 +158,22 @@ __device__ __forceinline__ uint4 bf16_pack(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// sigmoid(g) within a few units of 2^-23, 0 where exp(-g) overflows.
+// exp(-g) = 2^-(g hi) (1 - g lo ln 2) with log2 e = hi + lo: hi has 16 bits,
+// so that g hi is exact for the 8 bits of a bf16 gate and the 4 of a kept one
+// (rounded, with log2 e's own rounding, 4 units at g = -10 and 28 at -60), and
+// the rest is linear (its square is below 2^-23 where exp(-g) is finite).  32768 x
+// 2048 forward and backward: 105 and 144 us, 103 and 142 with __expf, 110 and
+// 147 with expf.
+__device__ __forceinline__ float sigmoid(float g) {
+  constexpr float kHi = 47274.f / 32768.f, kLoLn2 = 4.888495e-6f;
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -kHi));
+  e *= fmaxf(fmaf(g, -kLoLn2, 1.f), 0.f);
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // row groups
 // ---------------------------------------------------------------------------
@@ -188,6 +204,9 @@ __device__ __forceinline__ void ordered_offsets(int* offs, int E, int* status) {
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
+
+// Limit of a launch's waits for R rows times E matrices of N x K (train_api.cu).
+long long wait_limit_ns(int R, int N, int K, int E);
 
 moe_status quantize_blocks_launch(const void* x, bool f32, bool pow2, int rows, int cols, int64_t ldx,
                                   uint8_t* codes, float* scales, int num_sms, cudaStream_t s);

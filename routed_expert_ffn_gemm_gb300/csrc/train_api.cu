@@ -5,14 +5,6 @@
 #include "train.cuh"
 
 namespace moe {
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-cudaStream_t stream_of(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
-
-constexpr int kMaxExperts = 1024;
-constexpr int kMaxRows = 1 << 24;  // as T * k of the layer
 
 // How long the waits inside a launch may take, counted from its start: the
 // limit for a launch that gets stuck, and on top of it a long time for what a
@@ -28,6 +20,15 @@ long long wait_limit_ns(int R, int N, int K, int E) {
   const double nk = (double)N * K;
   return v + (long long)(2e-5 * R * nk + 2e-3 * E * nk);
 }
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+cudaStream_t stream_of(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxRows = 1 << 24;  // as T * k of the layer
 
 moe_status check_router_losses(int32_t T, int32_t E, int32_t k) {
   if (T < 0 || E <= 0 || k <= 0 || k > E) return MOE_ERR_INVALID_ARG;
