@@ -160,9 +160,9 @@ __device__ __forceinline__ void store_rows_m(const Params& p, const CUtensorMap*
 // Launches one cluster of CLUSTER CTAs for each unit, up to what is resident
 // at once: the grids are persistent, and not every SM finds its partners.
 // `known`: resident clusters per device, one value, written once.
-template <int CLUSTER, typename Kernel>
+template <int CLUSTER, typename Kernel, typename P, typename M>
 moe_status launch_clusters(Kernel kern, std::atomic<int> (&known)[64], int smem, long long units, int num_sms,
-                           cudaStream_t s, const Params& p, const Maps& maps) {
+                           cudaStream_t s, const P& p, const M& maps) {
   constexpr int kThreads = 384;
   int dev = 0;
   MOE_TRY_CUDA(cudaGetDevice(&dev));

@@ -4,11 +4,11 @@
 // the sums over all of K stay in tensor memory.
 //
 // A unit is 128 channels (the MMA's M side) x up to ROWS rows (N side) of one
-// expert.  Roles: warp 0 copies codes (TMA, 256 of the reduction a stage), warps
-// 2 and 3 bring the scales of weights and rows from where they lie into the
-// 512-byte atoms that the tensor cores take, warp 1 copies atoms to tensor
-// memory and issues the MMAs, warps 4..7 hold a quarter of the channels each and
-// write results.  Two accumulators, one filling while the other is written.
+// expert.  Roles: warp 0 copies codes and the weights' scales (TMA, 256 of the
+// reduction a stage), warp 3 brings the rows' scales into the 512-byte atoms
+// that the tensor cores take, warp 2 turns the weights' scales into atoms,
+// warp 1 copies atoms to tensor memory and issues the MMAs, warps 4..7 hold a
+// quarter of the channels each and write results.  Two accumulators, one filling while the other is written.
 #include "mxfp4_gemm.cuh"
 
 namespace moe {
@@ -17,8 +17,7 @@ namespace {
 using namespace mx_gemm;
 
 constexpr int kThreads = 256;
-constexpr int kWeightBytes = 128 * 128;
-constexpr int kAhead = 4;  // stages whose scales are on their way in registers
+constexpr int kWeightBytes = 128 * 128, kRawBytes = 8 * 128;
 
 template <int ROWS_>
 struct Tile {
@@ -27,9 +26,10 @@ struct Tile {
   static constexpr int STAGES = ROWS == 64 ? 8 : 6;
   static constexpr int STAGE_BYTES = kWeightBytes + ROWS * 128;
   static constexpr int SCALE_OFF = STAGES * STAGE_BYTES;     // [stage][weights 2, rows 2] atoms
-  static constexpr int BAR_OFF = SCALE_OFF + STAGES * 4 * kAtom;
-  // full[S], empty[S], acc_full[2], acc_empty[2], drain
-  static constexpr int NUM_BARS = 2 * STAGES + 5;
+  static constexpr int RAW_OFF = SCALE_OFF + STAGES * 4 * kAtom;  // weights' scales as copied
+  static constexpr int BAR_OFF = RAW_OFF + STAGES * kRawBytes;
+  // raw[S], full[S], empty[S], acc_full[2], acc_empty[2], drain
+  static constexpr int NUM_BARS = 3 * STAGES + 5;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NUM_BARS;
   static constexpr int ABORT_OFF = SLOT_OFF + 8;
   static constexpr int OFFS_OFF = ABORT_OFF + 8;
@@ -53,9 +53,10 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
   const uint32_t sbase = raw_s + pad, bars = sbase + T::BAR_OFF;
   auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
   auto empty_bar = [&](uint32_t s) { return bars + 8u * (T::STAGES + s); };
-  auto accf_bar = [&](uint32_t b) { return bars + 8u * (2 * T::STAGES + b); };
-  auto acce_bar = [&](uint32_t b) { return bars + 8u * (2 * T::STAGES + 2 + b); };
-  const uint32_t drain_bar = bars + 8u * (2 * T::STAGES + 4);
+  auto raw_bar = [&](uint32_t s) { return bars + 8u * (2 * T::STAGES + s); };
+  auto accf_bar = [&](uint32_t b) { return bars + 8u * (3 * T::STAGES + b); };
+  auto acce_bar = [&](uint32_t b) { return bars + 8u * (3 * T::STAGES + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (3 * T::STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::SLOT_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::ABORT_OFF);
   int* offs = reinterpret_cast<int*>(smem + T::OFFS_OFF);
@@ -66,7 +67,8 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::STAGES; ++s) {
-      ptx::mbar_init(full_bar(s), 3);  // the codes, the weights' and the rows' scales
+      ptx::mbar_init(raw_bar(s), 2);  // the weights' scales as copied, the rows' atoms
+      ptx::mbar_init(full_bar(s), 2);  // the codes, the scales' atoms
       ptx::mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -79,6 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
   }
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&maps.w);
+    ptx::prefetch_tmap(&maps.ws);
     for (int i = 0; i < T::BOXES; ++i) ptx::prefetch_tmap(&maps.a[i]);
   }
   if (warp == 1) {
@@ -95,7 +98,6 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
   const uint32_t tmem_base = *tmem_slot;
   const int units = prefix[p.E] * p.MT;
   const uint64_t deadline = ptx::globaltimer_ns() + (uint64_t)p.timeout_ns;
-  const long long steps = my_steps(u_first, u_step, units, p.KS);
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------- copies
@@ -114,7 +116,9 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
           ok = false;
           break;
         }
-        const uint32_t at = sbase + s * T::STAGE_BYTES, fb = full_bar(s);
+        const uint32_t at = sbase + s * T::STAGE_BYTES, fb = full_bar(s), rb = raw_bar(s);
+        ptx::mbar_arrive_expect_tx(rb, kRawBytes);
+        ptx::tma_load_box3(sbase + T::RAW_OFF + s * kRawBytes, &maps.ws, rb, x.mt * 128, ks * 8, x.g, pol);
         ptx::mbar_arrive_expect_tx(fb, bytes);
         ptx::tma_load_box3(at, &maps.w, fb, ks * 128, x.mt * 128, x.g, pol);
         ptx::tma_load_2d(at + kWeightBytes, &maps.a[box], fb, ks * 128, x.row0, keep);
@@ -125,12 +129,11 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
       ok = ptx::mbar_wait_bounded(empty_bar(j % T::STAGES), (j / T::STAGES) & 1u, deadline, abort_flag);
     if (!ok) {
       set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
-      // let issued copies land before shared memory is released (a stage
-      // whose scales never came does not complete: the limit ends the wait)
+      // let issued copies land before shared memory is released (a stage may
+      // never complete: the limit ends the wait)
       const uint64_t grace = ptx::globaltimer_ns() + 100000000ull;
-      for (uint32_t j = it > T::STAGES ? it - T::STAGES : 0; j < it; ++j)
-        while (!ptx::mbar_try_wait(full_bar(j % T::STAGES), (j / T::STAGES) & 1u) && ptx::globaltimer_ns() < grace) {
-        }
+      while (ptx::globaltimer_ns() < grace) {
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
@@ -174,54 +177,27 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
         }
       }
     }
-  } else if (warp == 2 || warp == 3) {
-    // ---------------------------------- scales: the weights' (2), the rows' (3)
-    constexpr int RW = ROWS / 32;  // rows of a lane: lane + 32 i
-    Walk<ROWS> w;
-    w.start(p, offs, prefix, u_first, u_step, units);
-    uint32_t v[kAhead][8];
-    auto load = [&](uint32_t (&to)[8]) {
-      if (!w.live()) return;
-      if (warp == 2) {
-        load_weight_scales(p, w.x.g, w.x.mt * 128 + 4 * lane, w.ks, to);
-      } else {
-#pragma unroll
-        for (int i = 0; i < RW; ++i) {
-          uint32_t r[2];
-          load_row_scales(p, lane + 32 * i < w.x.n_valid, (long long)w.x.row0 + lane + 32 * i, w.ks, r);
-          to[i] = r[0];
-          to[4 + i] = r[1];
-        }
-      }
-      w.next();
-    };
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0u;
-      load(v[j]);
-    }
+  } else if (warp == 2) {
+    // ------------------------- the weights' scales to atoms, once all have come
+    uint32_t it = 0;
     bool ok = true;
-    for (long long i0 = 0; i0 < steps && ok; i0 += kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const uint32_t it = (uint32_t)(i0 + j), s = it % T::STAGES;
-        if (!ok || i0 + j >= steps) break;
-        ok = warp_wait(empty_bar(s), ((it / T::STAGES) & 1u) ^ 1u, deadline, abort_flag);
+    for (int u = u_first; u < units && ok; u += u_step) {
+      for (int ks = 0; ks < p.KS; ++ks, ++it) {
+        const uint32_t s = it % T::STAGES;
+        ok = warp_wait(raw_bar(s), (it / T::STAGES) & 1u, deadline, abort_flag);
         if (!ok) break;
-        uint8_t* atoms = smem + T::SCALE_OFF + s * (4 * kAtom);
-        if (warp == 2) {
-          write_weight_scales(atoms, 4 * lane, v[j]);
-        } else {
-          *reinterpret_cast<uint4*>(atoms + 2 * kAtom + lane * 16) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
-          *reinterpret_cast<uint4*>(atoms + 3 * kAtom + lane * 16) = make_uint4(v[j][4], v[j][5], v[j][6], v[j][7]);
-        }
-        ptx::fence_proxy_async_smem();
+        weight_scale_atoms<128, kAtom>(smem + T::RAW_OFF + s * kRawBytes, smem + T::SCALE_OFF + s * (4 * kAtom));
+        ptx::fence_proxy_async_smem();  // (also for the rows' atoms, which the wait has seen)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(full_bar(s));
-        load(v[j]);
       }
     }
+    if (!ok && lane == 0) set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
+  } else if (warp == 3) {
+    // ---------------------------------------------------- the rows' scales
+    const bool ok = row_scales<ROWS, ROWS / 32, T::STAGES>(p, offs, prefix, u_first, u_step, units, 0,
+                                                           smem + T::SCALE_OFF + 2 * kAtom, 4 * kAtom, empty_bar, raw_bar,
+                                                           deadline, abort_flag);
     if (!ok && lane == 0) set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ results
@@ -289,6 +265,16 @@ moe_status launch(const Params& p, const Maps& maps, int num_sms, cudaStream_t s
 
 }  // namespace
 
+// From kMxManyRows rows an expert on average the product runs on
+// mxfp4_gemm_many.cu, up to kMxFewRows in tiles of 64 rows here, between in
+// tiles of 128.  64 experts of 7168 x 4096, us in tiles of 64, of 128 and there:
+// 16 rows 151, 154, 181; 48 rows 157, 158, 180; 64 rows 159, 160, 181 (spread
+// as rank^-0.6: 179, 170, 181); 96 rows 219, 173, 182; 128 rows 221, 187, 186
+// (277, 210, 192); 256 rows 424, 289, 196.  64 experts of 768 x 2048 with 128
+// rows: 46, 42, 30.  512 rows on 256 experts of 2048 x 7168: 288, 315, 346.  The
+// average counts experts without rows, which the host cannot see.
+constexpr long long kMxManyRows = 112, kMxFewRows = 32;
+
 moe_status mxfp4_gemm_launch(const MxGemmArgs& a, cudaStream_t s) {
   Params p{};
   p.R = a.R;
@@ -309,8 +295,17 @@ moe_status mxfp4_gemm_launch(const MxGemmArgs& a, cudaStream_t s) {
   if (((long long)a.R / 64 + a.E) * p.MT > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
   Maps maps;
   MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.N, a.K / 2, a.K / 2, 1, 128, 128, 128));
+  MOE_TRY(make_tmap_3d(&maps.ws, a.w_scales, a.E, p.KB, a.N, a.N, 1, 8, 128, 0));
   for (int i = 0; i < 5; ++i) MOE_TRY(make_tmap_2d(&maps.a[i], a.a, a.R, a.K / 2, 1, 8u << i, 128, 128));
-  const bool few = a.R <= 64 || (long long)a.R <= 48ll * a.E;
+  if ((long long)a.R >= kMxManyRows * a.E) {
+    const int es = a.out_f32 ? 4 : 2;
+    MOE_TRY(make_tmap_3d(&maps.out, a.out, 1, a.R, a.N, a.ld_out * es, es, 32, 64 / es, 64));
+    p.MT = ceil_div(a.N, 256);
+    MOE_TRY(make_tmap_3d(&maps.ws, a.w_scales, a.E, p.KB, a.N, a.N, 1, 8, 256, 0));
+    return mxfp4_gemm_many_launch(p, maps, a.num_sms, s);
+  }
+  // Few rows on average: more, smaller slots in flight.
+  const bool few = a.R <= 64 || (long long)a.R <= kMxFewRows * a.E;
   return few ? launch<64>(p, maps, a.num_sms, s) : launch<128>(p, maps, a.num_sms, s);
 }
 

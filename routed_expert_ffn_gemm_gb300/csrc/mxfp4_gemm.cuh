@@ -31,51 +31,19 @@ struct Params {
 struct Maps {
   CUtensorMap w;     // 128 channels x 128 bytes (256 codes)
   CUtensorMap a[5];  // boxes of 8 << i rows
+  CUtensorMap ws;    // weights' scales: 8 blocks of 128 channels (256 for a pair)
+  CUtensorMap out;   // 32 rows of 64 bytes (a pair's)
 };
 
-// How many stages this CTA (or pair) walks in all.
-__device__ __forceinline__ long long my_steps(int u_first, int u_step, int units, int KS) {
-  return u_first < units ? (long long)((units - 1 - u_first) / u_step + 1) * KS : 0;
-}
-
-// A walk over the stages of a CTA's units.
-template <int ROWS>
-struct Walk {
-  const int *offs, *prefix;
-  int E, MT, KS, units, u_step;
-  int u, ks;
-  Place x;
-  __device__ __forceinline__ void start(const Params& p, const int* o, const int* pre, int first, int step, int n) {
-    offs = o;
-    prefix = pre;
-    E = p.E;
-    MT = p.MT;
-    KS = p.KS;
-    units = n;
-    u_step = step;
-    u = first;
-    ks = 0;
-    if (u < units) x = place_of<ROWS>(u, offs, prefix, E, MT);
-  }
-  __device__ __forceinline__ bool live() const { return u < units; }
-  __device__ __forceinline__ void next() {
-    if (++ks < KS) return;
-    ks = 0;
-    u += u_step;
-    if (u < units) x = place_of<ROWS>(u, offs, prefix, E, MT);
-  }
-};
-
-// The lane's part of the scales of 128 channels x 8 blocks: channels
-// ch .. ch + 3 of each block (words along N; N % 16 == 0).  0 past the matrix.
-__device__ __forceinline__ void load_weight_scales(const Params& p, int g, int ch, int ks, uint32_t (&w)[8]) {
-  const uint8_t* from = p.w_scales + ((size_t)g * p.KB + (size_t)ks * 8) * p.N + ch;
+// The scales of 128 channels x 8 blocks from where a copy left them ([8 blocks]
+// [PITCH channels]) to two atoms `STEP` bytes apart: each lane turns four
+// channels' bytes of four blocks.
+template <int PITCH, int STEP>
+__device__ __forceinline__ void weight_scale_atoms(const uint8_t* raw, uint8_t* atoms) {
+  const int m = 4 * (threadIdx.x & 31);
+  uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j] = ch < p.N && ks * 8 + j < p.KB ? __ldg(reinterpret_cast<const uint32_t*>(from + (size_t)j * p.N)) : 0u;
-}
-// ... to two atoms: rows of the lane's four channels from `m` on.
-__device__ __forceinline__ void write_weight_scales(uint8_t* atoms, int m, const uint32_t (&w)[8]) {
+  for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint32_t*>(raw + j * PITCH + m);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t a = __byte_perm(w[4 * h], w[4 * h + 1], 0x5140), b = __byte_perm(w[4 * h + 2], w[4 * h + 3], 0x5140);
@@ -84,25 +52,121 @@ __device__ __forceinline__ void write_weight_scales(uint8_t* atoms, int m, const
                             __byte_perm(c, d, 0x7632)};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint32_t*>(atoms + h * kAtom + ((m + i) & 31) * 16 + ((m + i) >> 5) * 4) = of[i];
+      *reinterpret_cast<uint32_t*>(atoms + h * STEP + ((m + i) & 31) * 16 + ((m + i) >> 5) * 4) = of[i];
   }
 }
 
-// The scales of row `row` (8 blocks), 0 past its end or where it is not `live`.
-__device__ __forceinline__ void load_row_scales(const Params& p, bool live, long long row, int ks, uint32_t (&w)[2]) {
-  w[0] = w[1] = 0u;
+// Four words of a row's scales: the 16 blocks from `kb` on, by the widest loads
+// that the rows' alignment allows.  0 past the row's end and where it is not
+// `live` (blocks past K need any scale that is not NaN: their codes are 0).
+__device__ __forceinline__ void load_row_scales(const Params& p, bool live, long long row, int kb, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = 0u;
   if (!live) return;
-  const uint8_t* from = p.a_scales + (size_t)row * p.KB + (size_t)ks * 8;
-  const int n = p.KB - ks * 8;
-  if ((p.KB & 3) == 0) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(from));
-    if (n > 4) w[1] = __ldg(reinterpret_cast<const uint32_t*>(from) + 1);
+  const uint8_t* from = p.a_scales + (size_t)row * p.KB + kb;
+  const int left = p.KB - kb;
+  if ((p.KB & 15) == 0) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(from));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if ((p.KB & 7) == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (8 * i < left) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(from) + i);
+        w[2 * i] = v.x;
+        w[2 * i + 1] = v.y;
+      }
+  } else if ((p.KB & 3) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * i < left) w[i] = __ldg(reinterpret_cast<const uint32_t*>(from) + i);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) w[j >> 2] |= (uint32_t)__ldg(from + j) << (8 * (j & 3));
+    for (int j = 0; j < 16; ++j)
+      if (j < left) w[j >> 2] |= (uint32_t)__ldg(from + j) << (8 * (j & 3));
   }
+}
+
+// One warp: the scales of this CTA's rows (32 GROUPS of the unit's ROWS, from
+// `first` on) to two atoms a stage; lane 0's arrival on the stage's `raw` tells.
+// A lane holds rows lane + 32 i: a word of four blocks of each, side by side, is
+// 16 bytes of an atom.  Two stages' scales are one 16-byte load a row, kSets such
+// sets are on their way in registers.  The warp that loads must not fence: a
+// proxy fence waits for the loads in flight, which made each stage take the 1100
+// cycles of a load (16384 rows of 8 experts, 4096 -> 28672: 1120 us with loads in
+// front of the fence, 917 with 4-byte asynchronous copies, AFTER here).
+template <int ROWS, int GROUPS, int STAGES, typename Empty, typename Raw>
+__device__ __forceinline__ bool row_scales(const Params& p, const int* offs, const int* prefix, int u_first, int u_step,
+                                           int units, int first, uint8_t* atoms, int stage_bytes, Empty empty_bar,
+                                           Raw raw_bar, uint64_t deadline, volatile int* abort_flag) {
+  constexpr int kSets = 3;
+  const int lane = threadIdx.x & 31, pairs = (p.KS + 1) / 2;
+  int u = u_first, at = 0;  // what is loaded next
+  Place x;
+  x.row0 = x.n_valid = 0;
+  uint32_t v[kSets][GROUPS][4];
+  auto load = [&](uint32_t (&to)[GROUPS][4]) {
+    if (u >= units) return;
+    if (at == 0) x = place_of<ROWS>(u, offs, prefix, p.E, p.MT);
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+      const int r = first + lane + 32 * i;
+      load_row_scales(p, r < x.n_valid, (long long)x.row0 + r, 16 * at, to[i]);
+    }
+    if (++at == pairs) {
+      at = 0;
+      u += u_step;
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < kSets; ++j) {
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[j][i][k] = 0u;
+    load(v[j]);
+  }
+  const long long sets = u_first < units ? (long long)((units - 1 - u_first) / u_step + 1) * pairs : 0;
+  uint32_t it = 0;
+  int pair = 0;
+  bool ok = true;
+  for (long long i0 = 0; i0 < sets && ok; i0 += kSets) {
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      if (!ok || i0 + j >= sets) break;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!ok || 2 * pair + half >= p.KS) break;
+        const uint32_t s = it % STAGES;
+        ok = warp_wait(empty_bar(s), ((it / STAGES) & 1u) ^ 1u, deadline, abort_flag);
+        if (!ok) break;
+        ++it;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = i < GROUPS ? v[j][i % GROUPS][2 * half + h] : 0u;
+          uint8_t* to = atoms + s * stage_bytes + h * kAtom + lane * 16;
+          if constexpr (GROUPS > 2)
+            *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+          else
+            *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(raw_bar(s));
+      }
+      load(v[j]);
+      if (++pair == pairs) pair = 0;
+    }
+  }
+  return ok;
 }
 
 }  // namespace mx_gemm
+
+moe_status mxfp4_gemm_many_launch(const mx_gemm::Params& p, const mx_gemm::Maps& maps, int num_sms, cudaStream_t s);
+
 }  // namespace moe
