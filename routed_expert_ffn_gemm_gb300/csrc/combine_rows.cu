@@ -14,9 +14,11 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kGradThreads = 128;
-constexpr int kSlots = 8;  // rows of a token in flight
+constexpr int kItems = 64;         // forward: warps an SM for which a token's columns are shared out
+constexpr long long kMaxGrid = 1 << 20;
+constexpr int kTokenWarps = 16;  // backward: from this many tokens an SM on a warp takes a token, below a CTA
 
 // 16 bytes: 8 values of bf16 or 4 of fp32.
 template <bool F32>
@@ -48,145 +50,229 @@ __device__ __forceinline__ int row_at(const int32_t* inv, size_t a, int R, int* 
   return -1;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kThreads) combine_rows_kernel(const CombineRowsArgs p, long long pieces_all, int pieces) {
+// An item is a token's columns [part * span, (part + 1) * span) of 16 bytes, taken
+// by a warp: SLOTS rows and UNROLL pieces of each in flight.  ALL: k <= SLOTS,
+// the sums of a piece are done at once; else a piece at a time takes its rows in
+// groups of SLOTS.
+template <bool F32, int SLOTS, int UNROLL, bool ALL>
+__global__ void __launch_bounds__(kThreads) combine_rows_kernel(const CombineRowsArgs p, long long items, int parts,
+                                                                int span) {
+  static_assert(ALL || UNROLL == 1, "one piece's sums");
+  constexpr bool EARLY = SLOTS <= 4;  // add's loads go with the rows' (with eight rows they would cost occupancy)
   griddep_begin();
   using V = Vec<F32>;
   const int lane = threadIdx.x & 31, vecs = p.d / V::N;
   const uint4* rows = static_cast<const uint4*>(p.rows);
-  for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < pieces_all;
-       i += (long long)gridDim.x * (kThreads / 32)) {
-    const int t = (int)(i / pieces), at = (int)(i - (long long)t * pieces) * 32 + lane;
-    int r = -1;
-    float w = 1.f;
-    if (lane < p.k) {
-      r = row_at(p.inv_row, (size_t)t * p.k + lane, p.R, p.status);
-      if (p.w != nullptr && r >= 0) w = p.w[(size_t)t * p.k + lane];
-    }
-    const bool live = at < vecs;
-    float acc[V::N];
+  const uint4* add = static_cast<const uint4*>(p.add);  // (may be out)
+  const long long step = (long long)gridDim.x * (kThreads / 32);
+  for (long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += step) {
+    const int t = (int)(item / parts), part = (int)(item - (long long)t * parts);
+    int r[SLOTS];
+    float w[SLOTS];
+    auto slots = [&](int j0) {
 #pragma unroll
-    for (int c = 0; c < V::N; ++c) acc[c] = 0.f;
-    for (int j0 = 0; j0 < p.k; j0 += kSlots) {
-      uint4 q[kSlots];
-      int rj[kSlots];
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        rj[j] = j0 + j < p.k ? __shfl_sync(0xffffffffu, r, j0 + j) : -1;
-        if (live && rj[j] >= 0) q[j] = __ldg(rows + (size_t)rj[j] * vecs + at);
+      for (int j = 0; j < SLOTS; ++j) {
+        const size_t a = (size_t)t * p.k + j0 + j;
+        r[j] = j0 + j < p.k ? row_at(p.inv_row, a, p.R, p.status) : -1;
+        w[j] = r[j] >= 0 && p.w != nullptr ? p.w[a] : 1.f;
       }
+    };
+    if (ALL) slots(0);
+    const int end = min(vecs, (part + 1) * span);
+    for (int c0 = part * span + lane; c0 < end; c0 += 32 * UNROLL) {
+      uint4 q[UNROLL][SLOTS], more[UNROLL];
+      float acc[V::N];
+      auto load = [&] {
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-        if (live && rj[j] >= 0) {
-          float v[V::N];
-          V::values(q[j], v);
+        for (int i = 0; i < UNROLL; ++i) {
+          const int at = c0 + 32 * i;
+          if (at >= end) continue;
 #pragma unroll
-          for (int c = 0; c < V::N; ++c) acc[c] = fmaf(wj, v[c], acc[c]);
+          for (int j = 0; j < SLOTS; ++j)
+            if (r[j] >= 0) q[i][j] = __ldg(rows + (size_t)r[j] * vecs + at);
+          if (EARLY && add != nullptr) more[i] = add[(size_t)t * vecs + at];
         }
+      };
+      auto sum = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+          if (r[j] < 0) continue;
+          float v[V::N];
+          V::values(q[i][j], v);
+#pragma unroll
+          for (int c = 0; c < V::N; ++c) acc[c] = fmaf(w[j], v[c], acc[c]);
+        }
+      };
+      auto store = [&](int i) {
+        const size_t o = (size_t)t * vecs + c0 + 32 * i;
+        if (add != nullptr) {
+          float v[V::N];
+          V::values(EARLY ? more[i] : add[o], v);
+#pragma unroll
+          for (int c = 0; c < V::N; ++c) acc[c] += v[c];
+        }
+        static_cast<uint4*>(p.out)[o] = V::pack(acc);
+      };
+      if constexpr (ALL) {
+        load();
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+          if (c0 + 32 * i >= end) continue;
+#pragma unroll
+          for (int c = 0; c < V::N; ++c) acc[c] = 0.f;
+          sum(i);
+          store(i);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < V::N; ++c) acc[c] = 0.f;
+        for (int j0 = 0; j0 < p.k; j0 += SLOTS) {
+          slots(j0);
+          load();
+          sum(0);
+        }
+        store(0);
       }
     }
-    if (!live) continue;
-    const size_t o = (size_t)t * vecs + at;
-    if (p.add != nullptr) {
-      float v[V::N];
-      V::values(static_cast<const uint4*>(p.add)[o], v);  // (add may be out)
-#pragma unroll
-      for (int c = 0; c < V::N; ++c) acc[c] += v[c];
-    }
-    static_cast<uint4*>(p.out)[o] = V::pack(acc);
   }
 }
 
-template <bool F32, bool DROWS, bool DW>
+// SLOTS rows of a token at a time, UNROLL pieces of each in flight; WARPS warps
+// of the CTA share a token (1 or all of them).
+template <bool F32, bool DROWS, bool DW, int SLOTS, int UNROLL, int WARPS>
 __global__ void __launch_bounds__(kGradThreads) combine_rows_backward_kernel(const CombineRowsGradArgs p) {
   griddep_begin();
   using V = Vec<F32>;
-  constexpr int WARPS = kGradThreads / 32;
-  __shared__ float part[WARPS][kSlots];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vecs = p.d / V::N;
+  constexpr int GROUP = 32 * WARPS, TOKENS = kGradThreads / GROUP;
+  __shared__ float part[kGradThreads / 32][SLOTS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x % GROUP, vecs = p.d / V::N;
   const uint4* rows = static_cast<const uint4*>(p.rows);
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+  for (int t = blockIdx.x * TOKENS + threadIdx.x / GROUP; t < p.T; t += gridDim.x * TOKENS) {
     const uint4* dout = static_cast<const uint4*>(p.d_out) + (size_t)t * vecs;
-    for (int j0 = 0; j0 < p.k; j0 += kSlots) {
-      int r[kSlots];
-      float w[kSlots], dot[kSlots];
+    for (int j0 = 0; j0 < p.k; j0 += SLOTS) {
+      int r[SLOTS];
+      float w[SLOTS], dot[SLOTS];
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
+      for (int j = 0; j < SLOTS; ++j) {
         const size_t a = (size_t)t * p.k + j0 + j;
         r[j] = j0 + j < p.k ? row_at(p.inv_row, a, p.R, p.status) : -1;
         w[j] = DROWS && r[j] >= 0 && p.w != nullptr ? p.w[a] : 1.f;
         dot[j] = 0.f;
       }
-      for (int at = threadIdx.x; at < vecs; at += kGradThreads) {
-        float d[V::N];
-        const uint4 qd = dout[at];
-        uint4 q[kSlots];
-        if constexpr (DW) {
+      for (int at0 = me; at0 < vecs; at0 += GROUP * UNROLL) {
+        uint4 qd[UNROLL], q[UNROLL][SLOTS];
 #pragma unroll
-          for (int j = 0; j < kSlots; ++j)
-            if (r[j] >= 0) q[j] = __ldg(rows + (size_t)r[j] * vecs + at);
-        }
-        V::values(qd, d);
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-          if (r[j] < 0) continue;
+        for (int i = 0; i < UNROLL; ++i) {
+          const int at = at0 + GROUP * i;
+          if (at >= vecs) continue;
+          qd[i] = dout[at];
           if constexpr (DW) {
-            float v[V::N];
-            V::values(q[j], v);
 #pragma unroll
-            for (int c = 0; c < V::N; ++c) dot[j] = fmaf(d[c], v[c], dot[j]);
+            for (int j = 0; j < SLOTS; ++j)
+              if (r[j] >= 0) q[i][j] = __ldg(rows + (size_t)r[j] * vecs + at);
           }
-          if constexpr (DROWS) {
-            float v[V::N];
+        }
 #pragma unroll
-            for (int c = 0; c < V::N; ++c) v[c] = w[j] * d[c];
-            static_cast<uint4*>(p.d_rows)[(size_t)r[j] * vecs + at] = V::pack(v);
+        for (int i = 0; i < UNROLL; ++i) {
+          const int at = at0 + GROUP * i;
+          if (at >= vecs) continue;
+          float d[V::N];
+          V::values(qd[i], d);
+#pragma unroll
+          for (int j = 0; j < SLOTS; ++j) {
+            if (r[j] < 0) continue;
+            float v[V::N];
+            if constexpr (DW) {
+              V::values(q[i][j], v);
+#pragma unroll
+              for (int c = 0; c < V::N; ++c) dot[j] = fmaf(d[c], v[c], dot[j]);
+            }
+            if constexpr (DROWS) {
+#pragma unroll
+              for (int c = 0; c < V::N; ++c) v[c] = w[j] * d[c];
+              static_cast<uint4*>(p.d_rows)[(size_t)r[j] * vecs + at] = V::pack(v);
+            }
           }
         }
       }
       if constexpr (DW) {
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < SLOTS; ++j) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-          if (lane == 0) part[warp][j] = dot[j];
         }
-        __syncthreads();
-        const int j = (int)threadIdx.x;
-        if (j < kSlots && j0 + j < p.k) {
-          float sum = 0.f;
+        if constexpr (WARPS == 1) {
 #pragma unroll
-          for (int v = 0; v < WARPS; ++v) sum += part[v][j];
-          p.dw[(size_t)t * p.k + j0 + j] = sum;
+          for (int j = 0; j < SLOTS; ++j)
+            if (lane == j && j0 + j < p.k) p.dw[(size_t)t * p.k + j0 + j] = dot[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < SLOTS; ++j)
+            if (lane == 0) part[warp][j] = dot[j];
+          __syncthreads();
+          const int j = (int)threadIdx.x;
+          if (j < SLOTS && j0 + j < p.k) {
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < WARPS; ++v) sum += part[v][j];
+            p.dw[(size_t)t * p.k + j0 + j] = sum;
+          }
+          __syncthreads();
         }
-        __syncthreads();
       }
     }
   }
 }
 
-}  // namespace
-
-moe_status combine_rows_launch(const CombineRowsArgs& a, cudaStream_t s) {
-  const int pieces = ceil_div(a.d / (a.f32 ? 4 : 8), 32);
-  const long long all = (long long)a.T * pieces, want = (all + kThreads / 32 - 1) / (kThreads / 32);
-  const int grid = (int)(want < 16ll * a.num_sms ? want : 16ll * a.num_sms);
-  auto kern = a.f32 ? combine_rows_kernel<true> : combine_rows_kernel<false>;
-  MOE_TRY_CUDA(launch_k(kern, dim3(grid), dim3(kThreads), 0, s, a, all, pieces));
+template <bool F32, bool DROWS, bool DW>
+moe_status launch_backward(const CombineRowsGradArgs& a, cudaStream_t s) {
+  constexpr int ALL = kGradThreads / 32;
+  const bool wide = a.T < kTokenWarps * a.num_sms;  // few tokens: a CTA each
+  const int ctas = wide ? a.T : ceil_div(a.T, ALL), most = 64 * a.num_sms;
+  auto kern = a.k <= 2 ? (wide ? combine_rows_backward_kernel<F32, DROWS, DW, 2, 4, ALL> : combine_rows_backward_kernel<F32, DROWS, DW, 2, 4, 1>)
+              : a.k <= 4 ? (wide ? combine_rows_backward_kernel<F32, DROWS, DW, 4, 2, ALL> : combine_rows_backward_kernel<F32, DROWS, DW, 4, 2, 1>)
+                         : (wide ? combine_rows_backward_kernel<F32, DROWS, DW, 8, 1, ALL> : combine_rows_backward_kernel<F32, DROWS, DW, 8, 1, 1>);
+  MOE_TRY_CUDA(launch_k(kern, dim3(ctas < most ? ctas : most), dim3(kGradThreads), 0, s, a));
   return MOE_OK;
 }
 
+}  // namespace
+
+namespace {
+
+template <bool F32, int SLOTS, int UNROLL, bool ALL>
+moe_status launch_forward(const CombineRowsArgs& a, cudaStream_t s) {
+  // a warp a token, or a token's pieces over several warps where tokens are few
+  const int vecs = a.d / Vec<F32>::N, pieces = ceil_div(vecs, 32 * UNROLL);
+  const int parts = max(1, min(pieces, kItems * a.num_sms / a.T));
+  const int span = ceil_div(pieces, parts) * 32 * UNROLL;
+  const long long items = (long long)a.T * ceil_div(vecs, span);
+  const long long want = (items + kThreads / 32 - 1) / (kThreads / 32);
+  MOE_TRY_CUDA(launch_k(combine_rows_kernel<F32, SLOTS, UNROLL, ALL>, dim3((unsigned)(want < kMaxGrid ? want : kMaxGrid)),
+                        dim3(kThreads), 0, s, a, items, ceil_div(vecs, span), span));
+  return MOE_OK;
+}
+
+template <bool F32>
+moe_status launch_forward(const CombineRowsArgs& a, cudaStream_t s) {
+  if (a.k <= 1) return launch_forward<F32, 1, 4, true>(a, s);
+  if (a.k <= 2) return launch_forward<F32, 2, 4, true>(a, s);
+  if (a.k <= 4) return launch_forward<F32, 4, 2, true>(a, s);
+  return a.k <= 8 ? launch_forward<F32, 8, 1, true>(a, s) : launch_forward<F32, 8, 1, false>(a, s);
+}
+
+}  // namespace
+
+moe_status combine_rows_launch(const CombineRowsArgs& a, cudaStream_t s) {
+  return a.f32 ? launch_forward<true>(a, s) : launch_forward<false>(a, s);
+}
+
 moe_status combine_rows_backward_launch(const CombineRowsGradArgs& a, cudaStream_t s) {
-  const int grid = a.T < 32 * a.num_sms ? a.T : 32 * a.num_sms;
   const bool dr = a.d_rows != nullptr, dw = a.dw != nullptr;
   if (!dr && !dw) return MOE_OK;
-  auto kern = a.f32 ? (dr ? (dw ? combine_rows_backward_kernel<true, true, true> : combine_rows_backward_kernel<true, true, false>)
-                          : combine_rows_backward_kernel<true, false, true>)
-                    : (dr ? (dw ? combine_rows_backward_kernel<false, true, true> : combine_rows_backward_kernel<false, true, false>)
-                          : combine_rows_backward_kernel<false, false, true>);
-  MOE_TRY_CUDA(launch_k(kern, dim3(grid), dim3(kGradThreads), 0, s, a));
-  return MOE_OK;
+  if (a.f32)
+    return !dr ? launch_backward<true, false, true>(a, s) : dw ? launch_backward<true, true, true>(a, s) : launch_backward<true, true, false>(a, s);
+  return !dr ? launch_backward<false, false, true>(a, s) : dw ? launch_backward<false, true, true>(a, s) : launch_backward<false, true, false>(a, s);
 }
 
 }  // namespace moe

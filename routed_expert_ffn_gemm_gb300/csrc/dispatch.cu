@@ -257,16 +257,18 @@ __global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchA
   if ((int)threadIdx.x < n) {
     const int row = e < 0 ? -1 : cnt[warp * E + e] + rank;
     row_of[threadIdx.x] = row;
-    p.inv_row[a] = row;
-    if (row >= 0) p.row_token[row] = a / p.k;
-    if (a >= base[E]) p.row_token[a] = -1;
+    if (blockIdx.y == 0) {
+      p.inv_row[a] = row;
+      if (row >= 0) p.row_token[row] = a / p.k;
+      if (a >= base[E]) p.row_token[a] = -1;
+    }
   }
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int x = threadIdx.x; x <= E; x += kThreads) p.offsets[x] = base[x];
   if constexpr (M != kNone) {
     __syncthreads();
     const int pieces = pieces_of<M>(p), tokens = n / p.k, t0 = first / p.k;
-    for (int t = warp; t < tokens; t += WARPS)
+    for (int t = blockIdx.y * WARPS + warp; t < tokens; t += gridDim.y * WARPS)
 #pragma unroll 4
       for (int c = 0; c < pieces; ++c) move_piece<M, WIDE>(p, t0 + t, c, row_of + t * p.k);
   }
@@ -291,7 +293,10 @@ moe_status launch(const DispatchArgs& a, cudaStream_t s) {
   MOE_TRY_CUDA(launch_k(dispatch_count_kernel, dim3(n), dim3(kThreads), sizeof(int) * a.E, s, a, chunk));
   MOE_TRY_CUDA(launch_k(dispatch_scan_kernel, dim3(ceil_div(a.E, 32)), dim3(1024), 0, s, n, a.E, a.chunks, a.counts));
   const size_t smem = sizeof(int) * ((size_t)(kThreads / 32) * a.E + a.E + 1 + kChunkRows);
-  MOE_TRY_CUDA(launch_k(dispatch_move_kernel<M, WIDE>, dim3(n), dim3(kThreads), smem, s, a, chunk));
+  // chunks of few CTAs an SM end unevenly: several CTAs rank a chunk then, and
+  // each moves its share of the tokens
+  const int shares = M == kNone ? 1 : min(4, max(1, 16 * a.num_sms / n));
+  MOE_TRY_CUDA(launch_k(dispatch_move_kernel<M, WIDE>, dim3(n, shares), dim3(kThreads), smem, s, a, chunk));
   return MOE_OK;
 }
 

@@ -125,10 +125,8 @@ moe_status moe_quantize_mxfp4(int32_t rows, int32_t cols, int32_t x_dtype, int32
   if (rows == 0) return MOE_OK;
   if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(x) || !aligned(codes) || !aligned(scales)) return MOE_ERR_INVALID_ARG;
-  DeviceCtx ctx;
-  MOE_TRY(device_ctx(&ctx));
   return quantize_mxfp4_launch(x, x_dtype == MOE_F32, scale_kind == MOE_MX_FIT, rows, cols, matrix_rows, ld_x, codes,
-                               scales, ctx.num_sms, stream_of(stream));
+                               scales, stream_of(stream));
 }
 
 moe_status moe_mxfp4_values(int32_t rows, int32_t cols, int32_t dtype, int32_t matrix_rows, const uint8_t* codes,
@@ -137,9 +135,7 @@ moe_status moe_mxfp4_values(int32_t rows, int32_t cols, int32_t dtype, int32_t m
   if (rows == 0) return MOE_OK;
   if (codes == nullptr || scales == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(codes) || !aligned(scales) || !aligned(out)) return MOE_ERR_INVALID_ARG;
-  DeviceCtx ctx;
-  MOE_TRY(device_ctx(&ctx));
-  return mxfp4_values_launch(codes, scales, dtype == MOE_F32, rows, cols, matrix_rows, out, ctx.num_sms,
+  return mxfp4_values_launch(codes, scales, dtype == MOE_F32, rows, cols, matrix_rows, out,
                              stream_of(stream));
 }
 
@@ -151,10 +147,8 @@ moe_status moe_swiglu_mxfp4(int32_t R, int32_t ffn, int32_t scale_kind, const vo
   if (R == 0) return MOE_OK;
   if (g == nullptr || u == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(g) || !aligned(u) || !aligned(codes) || !aligned(scales) || !aligned(h)) return MOE_ERR_INVALID_ARG;
-  DeviceCtx ctx;
-  MOE_TRY(device_ctx(&ctx));
   SwigluMxArgs a{R, ffn, scale_kind == MOE_MX_FIT, g, u, ld, codes, scales, h};
-  return swiglu_mxfp4_launch(a, ctx.num_sms, stream_of(stream));
+  return swiglu_mxfp4_launch(a, stream_of(stream));
 }
 
 moe_status moe_grouped_mxfp4_gemm(int32_t R, int32_t K, int32_t N, int32_t E, int32_t out_dtype,

@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 32;  // rows and blocks of a tile of weights
+constexpr uint64_t kMaxGrid = 1 << 20;
 
 template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const uint8_t* __restrict__ x, uint32_t tasks,
@@ -171,10 +172,11 @@ __global__ void __launch_bounds__(kThreads) swiglu_mxfp4_kernel(const SwigluMxAr
   }
 }
 
-// CTAs for n of `each` a CTA: enough to fill the SMs with 8 CTAs each.
-int grid_of(uint64_t n, uint64_t each, int num_sms) {
-  const uint64_t want = (n + each - 1) / each, most = 8ull * (uint64_t)num_sms;
-  return (int)(want < most ? want : most);
+// CTAs for n of `each` a CTA, one round of them: a fixed grid of 8 CTAs an SM ends
+// in a round that is partly empty (SwiGLU of 65536 x 768: 5.05 rounds).
+unsigned grid_of(uint64_t n, uint64_t each) {
+  const uint64_t want = (n + each - 1) / each;
+  return (unsigned)(want < kMaxGrid ? want : kMaxGrid);
 }
 
 // Counts that, with a last partial step past them, have to fit 32 bits.
@@ -187,7 +189,7 @@ bool aligned32(const void* p, int64_t pitch_bytes) {
 }  // namespace
 
 moe_status quantize_mxfp4_launch(const void* x, bool f32, bool fit, int rows, int cols, int matrix_rows, int64_t ldx,
-                                 uint8_t* codes, uint8_t* scales, int num_sms, cudaStream_t s) {
+                                 uint8_t* codes, uint8_t* scales, cudaStream_t s) {
   const uint32_t nb = (uint32_t)(cols / kMxBlock);
   const uint64_t tasks = (uint64_t)rows * nb;
   if (!fits(tasks)) return MOE_ERR_UNSUPPORTED;
@@ -197,20 +199,20 @@ moe_status quantize_mxfp4_launch(const void* x, bool f32, bool fit, int rows, in
   if (matrix_rows == 0) {
     auto kern = f32 ? (wide ? quantize_rows_kernel<true, true> : quantize_rows_kernel<true, false>)
                     : (wide ? quantize_rows_kernel<false, true> : quantize_rows_kernel<false, false>);
-    MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tasks, kThreads, num_sms)), dim3(kThreads), 0, s, xb, (uint32_t)tasks, nb,
+    MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tasks, kThreads)), dim3(kThreads), 0, s, xb, (uint32_t)tasks, nb,
                           ldx, (int)fit, cb, scales));
     return MOE_OK;
   }
   const uint64_t tiles = (uint64_t)(rows / matrix_rows) * ceil_div(matrix_rows, kTile) * ceil_div((int)nb, kTile);
   auto kern = f32 ? (wide ? quantize_weights_kernel<true, true> : quantize_weights_kernel<true, false>)
                   : (wide ? quantize_weights_kernel<false, true> : quantize_weights_kernel<false, false>);
-  MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tiles, 1, num_sms)), dim3(kThreads), 0, s, xb, (uint32_t)tiles, nb,
+  MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tiles, 1)), dim3(kThreads), 0, s, xb, (uint32_t)tiles, nb,
                         (uint32_t)matrix_rows, ldx, (int)fit, cb, scales));
   return MOE_OK;
 }
 
 moe_status mxfp4_values_launch(const uint8_t* codes, const uint8_t* scales, bool f32, int rows, int cols,
-                               int matrix_rows, void* out, int num_sms, cudaStream_t s) {
+                               int matrix_rows, void* out, cudaStream_t s) {
   const uint32_t nb = (uint32_t)(cols / kMxBlock);
   const uint64_t tasks = (uint64_t)rows * nb;
   if (!fits(tasks)) return MOE_ERR_UNSUPPORTED;
@@ -220,25 +222,25 @@ moe_status mxfp4_values_launch(const uint8_t* codes, const uint8_t* scales, bool
   if (matrix_rows == 0) {
     auto kern = f32 ? (wide ? row_values_kernel<true, true> : row_values_kernel<true, false>)
                     : (wide ? row_values_kernel<false, true> : row_values_kernel<false, false>);
-    MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tasks, kThreads, num_sms)), dim3(kThreads), 0, s, cb, scales,
+    MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tasks, kThreads)), dim3(kThreads), 0, s, cb, scales,
                           (uint32_t)tasks, ob));
     return MOE_OK;
   }
   const uint64_t tiles = (uint64_t)(rows / matrix_rows) * ceil_div(matrix_rows, kTile) * ceil_div((int)nb, kTile);
   auto kern = f32 ? (wide ? weight_values_kernel<true, true> : weight_values_kernel<true, false>)
                   : (wide ? weight_values_kernel<false, true> : weight_values_kernel<false, false>);
-  MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tiles, 1, num_sms)), dim3(kThreads), 0, s, cb, scales, (uint32_t)tiles, nb,
+  MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tiles, 1)), dim3(kThreads), 0, s, cb, scales, (uint32_t)tiles, nb,
                         (uint32_t)matrix_rows, ob));
   return MOE_OK;
 }
 
-moe_status swiglu_mxfp4_launch(const SwigluMxArgs& a, int num_sms, cudaStream_t s) {
+moe_status swiglu_mxfp4_launch(const SwigluMxArgs& a, cudaStream_t s) {
   const uint32_t nb = (uint32_t)(a.f / kMxBlock);
   const uint64_t tasks = (uint64_t)a.R * nb;
   if (!fits(tasks)) return MOE_ERR_UNSUPPORTED;
   const bool wide = aligned32(a.g, a.ld * 2) && aligned32(a.u, 0);
   auto kern = wide ? swiglu_mxfp4_kernel<true> : swiglu_mxfp4_kernel<false>;
-  MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tasks, kThreads, num_sms)), dim3(kThreads), 0, s, a, (uint32_t)tasks, nb));
+  MOE_TRY_CUDA(launch_k(kern, dim3(grid_of(tasks, kThreads)), dim3(kThreads), 0, s, a, (uint32_t)tasks, nb));
   return MOE_OK;
 }
 

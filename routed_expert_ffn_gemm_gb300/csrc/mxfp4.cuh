@@ -150,9 +150,9 @@ struct MxBlock {
 // ---------------------------------------------------------------------------
 
 moe_status quantize_mxfp4_launch(const void* x, bool f32, bool fit, int rows, int cols, int matrix_rows, int64_t ldx,
-                                 uint8_t* codes, uint8_t* scales, int num_sms, cudaStream_t s);
+                                 uint8_t* codes, uint8_t* scales, cudaStream_t s);
 moe_status mxfp4_values_launch(const uint8_t* codes, const uint8_t* scales, bool f32, int rows, int cols,
-                               int matrix_rows, void* out, int num_sms, cudaStream_t s);
+                               int matrix_rows, void* out, cudaStream_t s);
 
 struct SwigluMxArgs {
   int R, f;
@@ -164,7 +164,7 @@ struct SwigluMxArgs {
   uint8_t* scales;
   void* h;  // nullable
 };
-moe_status swiglu_mxfp4_launch(const SwigluMxArgs& a, int num_sms, cudaStream_t s);
+moe_status swiglu_mxfp4_launch(const SwigluMxArgs& a, cudaStream_t s);
 
 struct DispatchArgs {
   int T, d, E, k;

@@ -98,41 +98,46 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
   const uint32_t tmem_base = *tmem_slot;
   const int units = prefix[p.E] * p.MT;
   const uint64_t deadline = ptx::globaltimer_ns() + (uint64_t)p.timeout_ns;
+  Units<ROWS> places(p, offs, prefix);
 
-  if (warp == 0 && lane == 0) {
-    // ---------------------------------------------------------- copies
+  if (warp == 0) {
+    // ---------------------------------------------------------- copies (lane 0)
     const uint64_t once = ptx::policy_evict_first(), keep = ptx::policy_evict_normal();
     uint32_t it = 0;
     bool ok = true;
     for (int u = u_first; u < units && ok; u += u_step) {
-      const Place x = place_of<ROWS>(u, offs, prefix, p.E, p.MT);
+      const Place x = places.at(u);
       int box = 0;  // the box holds the rows; what the MMA reads past it is any earlier stage's, in columns that nobody stores
       while (box < T::BOXES - 1 && x.n_valid > 8 << box) ++box;
       const uint32_t bytes = kWeightBytes + (8u << box) * 128u;
       const uint64_t pol = x.tiles > 1 ? keep : once;
-      for (int ks = 0; ks < p.KS; ++ks, ++it) {
-        const uint32_t s = it % T::STAGES;
-        if (!ptx::mbar_wait_bounded(empty_bar(s), ((it / T::STAGES) & 1u) ^ 1u, deadline, abort_flag)) {
-          ok = false;
-          break;
+      if (lane == 0)
+        for (int ks = 0; ks < p.KS; ++ks, ++it) {
+          const uint32_t s = it % T::STAGES;
+          if (!ptx::mbar_wait_bounded(empty_bar(s), ((it / T::STAGES) & 1u) ^ 1u, deadline, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = sbase + s * T::STAGE_BYTES, fb = full_bar(s), rb = raw_bar(s);
+          ptx::mbar_arrive_expect_tx(rb, kRawBytes);
+          ptx::tma_load_box3(sbase + T::RAW_OFF + s * kRawBytes, &maps.ws, rb, x.mt * 128, ks * 8, x.g, pol);
+          ptx::mbar_arrive_expect_tx(fb, bytes);
+          ptx::tma_load_box3(at, &maps.w, fb, ks * 128, x.mt * 128, x.g, pol);
+          ptx::tma_load_2d(at + kWeightBytes, &maps.a[box], fb, ks * 128, x.row0, keep);
         }
-        const uint32_t at = sbase + s * T::STAGE_BYTES, fb = full_bar(s), rb = raw_bar(s);
-        ptx::mbar_arrive_expect_tx(rb, kRawBytes);
-        ptx::tma_load_box3(sbase + T::RAW_OFF + s * kRawBytes, &maps.ws, rb, x.mt * 128, ks * 8, x.g, pol);
-        ptx::mbar_arrive_expect_tx(fb, bytes);
-        ptx::tma_load_box3(at, &maps.w, fb, ks * 128, x.mt * 128, x.g, pol);
-        ptx::tma_load_2d(at + kWeightBytes, &maps.a[box], fb, ks * 128, x.row0, keep);
-      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
-    // every slot's last arrival, too, before the CTA may leave
-    for (uint32_t j = it > T::STAGES ? it - T::STAGES : 0; j < it && ok; ++j)
-      ok = ptx::mbar_wait_bounded(empty_bar(j % T::STAGES), (j / T::STAGES) & 1u, deadline, abort_flag);
-    if (!ok) {
-      set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
-      // let issued copies land before shared memory is released (a stage may
-      // never complete: the limit ends the wait)
-      const uint64_t grace = ptx::globaltimer_ns() + 100000000ull;
-      while (ptx::globaltimer_ns() < grace) {
+    if (lane == 0) {
+      // every slot's last arrival, too, before the CTA may leave
+      for (uint32_t j = it > T::STAGES ? it - T::STAGES : 0; j < it && ok; ++j)
+        ok = ptx::mbar_wait_bounded(empty_bar(j % T::STAGES), (j / T::STAGES) & 1u, deadline, abort_flag);
+      if (!ok) {
+        set_device_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
+        // let issued copies land before shared memory is released (a stage may
+        // never complete: the limit ends the wait)
+        const uint64_t grace = ptx::globaltimer_ns() + 100000000ull;
+        while (ptx::globaltimer_ns() < grace) {
+        }
       }
     }
   } else if (warp == 1) {
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
     uint32_t it = 0, n = 0;
     bool ok = true;
     for (int u = u_first; u < units && ok; u += u_step, ++n) {
-      const Place x = place_of<ROWS>(u, offs, prefix, p.E, p.MT);
+      const Place x = places.at(u);
       const int n_mma = __shfl_sync(0xffffffffu, (x.n_valid + 31) / 32 * 32, 0);
       const uint32_t idesc[2] = {ptx::idesc_mxf4(128, n_mma, 0), ptx::idesc_mxf4(128, n_mma, 1)};
       const uint32_t b = n & 1u, d = tmem_base + kAccCols * b;
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
     uint32_t n = 0;
     bool ok = true;
     for (int u = u_first; u < units; u += u_step, ++n) {
-      const Place x = place_of<ROWS>(u, offs, prefix, p.E, p.MT);
+      const Place x = places.at(u);
       const uint32_t b = n & 1u;
       ok = warp_wait(accf_bar(b), (n >> 1) & 1u, deadline, abort_flag);
       if (!ok) break;
@@ -215,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
       const bool live = ch < p.N;
       for (int c = 0; c < x.n_valid; c += 32) {
         uint32_t d[32];
+        __syncwarp();
         ptx::tmem_ld32(at + kAccCols * b + c, d);
         ptx::tmem_ld_wait();
         if (c + 32 >= x.n_valid) {  // everything is in registers: the accumulator can fill again

@@ -8,8 +8,8 @@ namespace moe {
 namespace mx_gemm {
 
 using block_gemm::Place;
+using block_gemm::kBand;
 using block_gemm::kMaxGroups;
-using block_gemm::place_of;
 using block_gemm::row_tiles;
 using block_gemm::warp_wait;
 
@@ -33,6 +33,53 @@ struct Maps {
   CUtensorMap a[5];  // boxes of 8 << i rows
   CUtensorMap ws;    // weights' scales: 8 blocks of 128 channels (256 for a pair)
   CUtensorMap out;   // 32 rows of 64 bytes (a pair's)
+};
+
+// 2^32 / n rounded up, n from 2 to kBand.
+static_assert(kBand == 16, "kInverse");
+static __constant__ const unsigned kInverse[kBand + 1] = {
+    0u,          0u,          0x80000000u, 0x55555556u, 0x40000000u,
+    0x33333334u, 0x2aaaaaabu, 0x24924925u, 0x20000000u, 0x1c71c71du,
+    0x1999999au, 0x1745d175u, 0x15555556u, 0x13b13b14u,
+    0x12492493u, 0x11111112u, 0x10000000u};
+
+// Where a warp's units are, asked in ascending order: block_gemm's place_of (row
+// tiles of ROWS rows first inside bands of kBand) in some 100 cycles instead of
+// 1200, which every role would spend on every unit (65536 rows on 128 experts of
+// 768 x 2048, three stages a unit: 88 us before, AFTER here).  The expert is
+// sought from the last one on by all lanes at once, and the one division left is
+// by a number up to kBand.
+template <int ROWS>
+struct Units {
+  const int *offs, *prefix;
+  int E, MT, g;
+  __device__ __forceinline__ Units(const Params& p, const int* o, const int* pre) : offs(o), prefix(pre), E(p.E), MT(p.MT), g(0) {}
+
+  // (the whole warp)
+  __device__ __forceinline__ Place at(int u) {
+    const int lane = threadIdx.x & 31;
+    for (;;) {  // the last expert that begins at or before u
+      const int next = g + 1 + lane;
+      const int n = __popc(__ballot_sync(0xffffffffu, next < E && prefix[min(next, E)] * MT <= u));
+      g += n;
+      if (n < 32) break;
+    }
+    Place x;
+    x.g = g;
+    x.tiles = prefix[g + 1] - prefix[g];
+    int rem = u - prefix[g] * MT, tile0 = 0;
+    if (x.tiles > kBand) {
+      tile0 = rem / (kBand * MT) * kBand;
+      rem -= tile0 * MT;
+    }
+    const int wide = min(kBand, x.tiles - tile0);
+    // rem / wide: exact by a multiplication with 2^32 / wide rounded up, as
+    // rem * kBand < 2^32
+    x.mt = wide == 1 ? rem : (int)__umulhi((unsigned)rem, kInverse[wide]);
+    x.row0 = offs[g] + (tile0 + rem - x.mt * wide) * ROWS;
+    x.n_valid = min(ROWS, offs[g + 1] - x.row0);
+    return x;
+  }
 };
 
 // The scales of 128 channels x 8 blocks from where a copy left them ([8 blocks]
@@ -105,12 +152,13 @@ __device__ __forceinline__ bool row_scales(const Params& p, const int* offs, con
   constexpr int kSets = 3;
   const int lane = threadIdx.x & 31, pairs = (p.KS + 1) / 2;
   int u = u_first, at = 0;  // what is loaded next
+  Units<ROWS> places(p, offs, prefix);
   Place x;
   x.row0 = x.n_valid = 0;
   uint32_t v[kSets][GROUPS][4];
   auto load = [&](uint32_t (&to)[GROUPS][4]) {
     if (u >= units) return;
-    if (at == 0) x = place_of<ROWS>(u, offs, prefix, p.E, p.MT);
+    if (at == 0) x = places.at(u);
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) {
       const int r = first + lane + 32 * i;

@@ -98,16 +98,17 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_many_kernel(const Para
   const uint32_t tmem_base = *tmem_slot;
   const int units = prefix[p.E] * p.MT;
   const uint64_t deadline = ptx::globaltimer_ns() + (uint64_t)p.timeout_ns;
+  Units<256> places(p, offs, prefix);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- copies
-      const uint64_t keep = ptx::policy_evict_normal();
-      uint32_t it = 0;
-      bool ok = true;
-      for (int u = u_first; u < units && ok; u += u_step) {
-        const Place x = place_of<256>(u, offs, prefix, p.E, p.MT);
-        const int row = x.row0 + (int)rank * 128, ch = x.mt * 256 + (int)rank * 128;
+    // ---------------------------------------------------------- copies (lane 0)
+    const uint64_t keep = ptx::policy_evict_normal();
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = u_first; u < units && ok; u += u_step) {
+      const Place x = places.at(u);
+      const int row = x.row0 + (int)rank * 128, ch = x.mt * 256 + (int)rank * 128;
+      if (lane == 0)
         for (int ks = 0; ks < p.KS; ++ks, ++it) {
           const uint32_t s = it % kStages;
           if (!ptx::mbar_wait_bounded(empty_bar(s), ((it / kStages) & 1u) ^ 1u, deadline, abort_flag)) {
@@ -121,7 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_many_kernel(const Para
           ptx::tma_load_2d_pair(at, &maps.a[4], fb, ks * 128, row, keep);
           ptx::tma_load_box3_pair(at + kTileBytes, &maps.w, fb, ks * 128, ch, x.g, keep);
         }
-      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    }
+    if (lane == 0) {
       // every slot's last arrival from the even CTA, too, before the CTA may leave
       for (uint32_t j = it > kStages ? it - kStages : 0; j < it && ok; ++j)
         ok = ptx::mbar_wait_bounded(empty_bar(j % kStages), (j / kStages) & 1u, deadline, abort_flag);
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_many_kernel(const Para
     uint32_t n = 0, buf = 0;
     bool ok = true;
     for (int u = u_first; u < units; u += u_step, ++n) {
-      const Place x = place_of<256>(u, offs, prefix, p.E, p.MT);
+      const Place x = places.at(u);
       const uint32_t b = n & 1u;
       ok = warp_wait(accf_bar(b), (n >> 1) & 1u, deadline, abort_flag);
       if (!ok) break;
@@ -233,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_many_kernel(const Para
       for (int t = 0; t < 4; ++t) {
         const int c = down ? 3 - t : t, ch0 = x.mt * 256 + h * 128 + 32 * c;
         uint32_t d[32];
+        __syncwarp();
         if (t == 0 || (r0 < x.n_valid && ch0 < p.N)) {
           ptx::tmem_ld32(at + kAccStep * b + 32 * c, d);
           ptx::tmem_ld_wait();
