@@ -8,8 +8,8 @@ fp32 master weights are kept; after each step the experts are laid out again
 as E4M3 codes with a scale for each 128 x 128 block (gate and up as one
 matrix).  For the backward pass a step keeps the token rows, the gate and the
 up activations in 8 bits and nothing else of the experts.  The elementwise
-glue between the library's calls (the loss, the gradients of the combine) is
-plain torch.
+glue around the library's calls (the loss, the router's product) is plain
+torch.
 """
 
 import argparse
@@ -60,28 +60,21 @@ class Layer:
         new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
         logits, idx, w = new(T, E, dtype=torch.float32), new(T, k, dtype=torch.int32), new(T, k, dtype=torch.float32)
         api.moe_router_topk(p, x, self.w_router, None, None, logits, idx, w)
-        counts, offsets = new(E, dtype=torch.int32), new(E + 1, dtype=torch.int32)
-        token, row, x_rows = new(T * k, dtype=torch.int32), new(T * k, dtype=torch.int32), new(T * k, d, dtype=x.dtype)
-        api.moe_permute(p, idx, x, counts, offsets, token, row, x_rows, api.workspace_for(p))
+        moved = api.dispatch(x, idx, E)
+        offsets, row = moved.offsets, moved.inv_row
         # powers of two: the same codes are the weight gradient's checkpoint
-        x_codes, x_scales = api.quantize_blocks(x_rows, "pow2")
+        x_codes, x_scales = api.quantize_blocks(moved.rows, "pow2")
         gu = api.grouped_block_gemm(x_codes, x_scales, offsets, self.q_gu, self.s_gu)
         h = api.swiglu_save(gu[:, :f], gu[:, f:])
         y = api.grouped_block_gemm(h.codes, h.scales, offsets, self.q_down, self.s_down)
-        out = torch.empty_like(x)
-        api.moe_combine(p, y, row, w, None, out)
+        out = api.combine(y, row, w)
         losses = api.router_losses(logits, idx, balance, z)
-        return out, losses, (p, x, logits, idx, w, offsets, token, row, x_codes, x_scales, h.saved, h.saved_scales, y)
+        return out, losses, (p, x, logits, idx, w, offsets, row, x_codes, x_scales, h.saved, h.saved_scales, y)
 
     def backward(self, d_out, losses, kept):
         """Gradients of x, w_gu, w_down and w_router from d_out [T, d] bf16."""
-        p, x, logits, idx, w, offsets, token, row, x_codes, x_scales, saved, saved_scales, y = kept
-        T, k = idx.shape
-        # the combine's gradients
-        flat = w.new_empty(T * k)
-        flat[row.long()] = w.view(-1)
-        dy = (d_out[token.long()] * flat[:, None]).bfloat16()
-        d_w = (y[row.long()].view(T, k, -1).float() * d_out[:, None].float()).sum(2)
+        p, x, logits, idx, w, offsets, row, x_codes, x_scales, saved, saved_scales, y = kept
+        dy, d_w = api.combine_backward(d_out, y, row, w)
         # the experts'
         dy_codes, dy_scales = api.quantize_blocks(dy, "amax")
         dh = api.grouped_block_gemm(dy_codes, dy_scales, offsets, self.q_down, self.s_down, transposed=True)
@@ -89,8 +82,7 @@ class Layer:
         d_down = api.grouped_wgrad(dy, g.h, None, offsets)
         d_gu = api.grouped_wgrad(g.d_gu, x_codes, x_scales, offsets)
         dx_rows = api.grouped_block_gemm(g.codes, g.scales, offsets, self.q_gu, self.s_gu, transposed=True)
-        dx = torch.empty_like(x)
-        api.moe_combine(p, dx_rows, row, torch.ones_like(w), None, dx)
+        dx = api.dispatch_backward(dx_rows, row)
         # the router's
         d_logits = api.router_losses_backward(logits, idx, losses, topk_w=w, d_topk_w=d_w)
         dx = (dx.float() + d_logits @ self.w_router.float()).bfloat16()

@@ -234,6 +234,18 @@ def _call(name, *args):
         raise MoEError(name, st)
 
 
+@functools.lru_cache(maxsize=None)
+def _fn(name):
+    return getattr(_lib(), name)
+
+
+def _run(name, *args):
+    """_call with the entry point looked up once (a quarter of a microsecond)."""
+    st = _fn(name)(*args)
+    if st != OK:
+        raise MoEError(name, st)
+
+
 def moe_router_topk(p, x, w_router, router_bias, logits_in, logits_out, topk_idx, topk_w, stream=None):
     a = _act_size(p)
     _check(x, "x", p.T * p.d, a)
@@ -725,12 +737,25 @@ def _mx_scale(kind) -> int:
     return MX_SCALE[kind]
 
 
-def _here(*tensors) -> None:
+def _here(t: torch.Tensor, *more) -> None:
     """The tensors are on the current device: the kernels run there."""
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor on {t.device}, the current device is cuda:{dev}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the library takes device tensors")
+    for o in more:
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors on {t.device} and {o.device}")
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"tensors on {t.device}, which is not the current device")
+
+
+def _at(t: Optional[torch.Tensor]):
+    """The address of a tensor that _here has seen."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 class Dispatched(NamedTuple):
@@ -768,9 +793,10 @@ def moe_dispatch_workspace_size(T: int, E: int, k: int) -> int:
 
 
 def _slots(idx, name) -> tuple:
-    if idx.dim() != 2 or idx.dtype is not torch.int32:
-        raise ValueError(f"{name}: {idx.dtype} {list(idx.shape)}, the call takes torch.int32 [T, k]")
-    return tuple(idx.shape)
+    shape = idx.shape
+    if len(shape) != 2 or idx.dtype is not torch.int32:
+        raise ValueError(f"{name}: {idx.dtype} {list(shape)}, the call takes torch.int32 [T, k]")
+    return shape
 
 
 def dispatch(x, topk_idx, E, quantize=None, rows=None, scales=None, workspace=None, stream=None) -> Dispatched:
@@ -780,45 +806,44 @@ def dispatch(x, topk_idx, E, quantize=None, rows=None, scales=None, workspace=No
     if stream is not None:
         return _on_stream(stream, dispatch, x, topk_idx, E, quantize, rows, scales, workspace)
     T, k = _slots(topk_idx, "topk_idx")
-    _here(x, topk_idx, rows, scales, workspace)
     R, dev, empty = T * k, topk_idx.device, torch.empty
-    d, ld, kind, out_kind, mx = 8, 8, DTYPE["bf16"], DTYPE["bf16"], 0
+    size = moe_dispatch_workspace_size(T, E, k)  # (refuses sizes)
     if x is None:
         if quantize is not None or rows is not None or scales is not None:
             raise ValueError("rows: there are none without x")
+        d, ld, kind, out_kind, mx, at = 8, 8, 1, 1, 0, None
     else:
-        ld = _rows(x, "x")
-        kind = out_kind = _type(x.dtype, "x")
-        d = x.shape[1]
-        if x.shape[0] != T:
-            raise ValueError(f"x: {list(x.shape)}, topk_idx has {T} tokens")
-        if quantize is None:
-            shape, t = (R, d), x.dtype
-            if scales is not None:
-                raise ValueError("scales: there are none without quantize")
-        else:
-            mx, out_kind = _mx_scale(quantize), DTYPE["mxfp4"]
+        ld, kind, at, mx = _rows(x, "x"), _type(x.dtype, "x"), x.data_ptr(), 0
+        n, d = x.shape
+        if n != T:
+            raise ValueError(f"x: {[n, d]}, topk_idx has {T} tokens")
+        shape, t, out_kind = (R, d), x.dtype, kind
+        if quantize is not None:
             if d % MX_BLOCK:
                 raise ValueError(f"x: {d} columns are no multiple of {MX_BLOCK}")
-            shape, t = (R, d // 2), torch.uint8
-            if scales is None:
-                scales = empty((R, d // MX_BLOCK), dtype=torch.uint8, device=dev)
-            else:
-                _exact(scales, "scales", (R, d // MX_BLOCK), torch.uint8)
+            shape, t, out_kind, mx = (R, d // 2), torch.uint8, DTYPE["mxfp4"], _mx_scale(quantize)
+            _exact(scales, "scales", (R, d // MX_BLOCK), torch.uint8)
+        elif scales is not None:
+            raise ValueError("scales: there are none without quantize")
+        _exact(rows, "rows", shape, t)
+    _here(topk_idx, x, rows, scales, workspace)
+    if x is not None:
         if rows is None:
             rows = empty(shape, dtype=t, device=dev)
-        else:
-            _exact(rows, "rows", shape, t)
+        if scales is None and quantize is not None:
+            scales = empty((R, d // MX_BLOCK), dtype=torch.uint8, device=dev)
+    # (four allocations: one with four views of it takes 6 us of host time more)
     offsets = empty(E + 1, dtype=torch.int32, device=dev)
     counts = empty(E, dtype=torch.int32, device=dev)
     row_token = empty(R, dtype=torch.int32, device=dev)
-    inv_row = empty((T, k), dtype=torch.int32, device=dev)
+    inv_row = torch.empty_like(topk_idx, memory_format=torch.contiguous_format)
     if workspace is None:
-        n = moe_dispatch_workspace_size(T, E, k)
-        workspace = empty(n, dtype=torch.uint8, device=dev) if n else None
-    _call("moe_dispatch", T, d, E, k, kind, out_kind, mx, None if x is None else _pitched(x), ld, _ptr(topk_idx),
-          _ptr(counts), _ptr(offsets), _ptr(row_token), _ptr(inv_row), _ptr(rows), _ptr(scales), _ptr(workspace),
-          0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(None))
+        if size:
+            workspace = empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _run("moe_dispatch", T, d, E, k, kind, out_kind, mx, at, ld, _at(topk_idx), counts.data_ptr(), offsets.data_ptr(),
+         row_token.data_ptr(), inv_row.data_ptr(), _at(rows), _at(scales), _at(workspace), size, _stream(None))
     return Dispatched(rows, scales, offsets, counts, row_token, inv_row)
 
 
@@ -831,14 +856,15 @@ def combine(y, inv_row, topk_w=None, add=None, out=None, stream=None):
     if y.dim() != 2:
         raise ValueError("y: [R, d] is expected")
     _here(y, inv_row, topk_w, add, out)
-    (R, d), kind = y.shape, _type(y.dtype, "y")
+    (R, d), dtype = y.shape, y.dtype
+    kind = _type(dtype, "y")
     _exact(topk_w, "topk_w", (T, k), torch.float32)
-    _exact(add, "add", (T, d), y.dtype)
+    _exact(add, "add", (T, d), dtype)
     if out is None:
-        out = torch.empty((T, d), dtype=y.dtype, device=y.device)
+        out = torch.empty((T, d), dtype=dtype, device=y.device)
     else:
-        _exact(out, "out", (T, d), y.dtype)
-    _call("moe_combine_rows", T, d, k, R, kind, _ptr(y), _ptr(inv_row), _ptr(topk_w), _ptr(add), _ptr(out), _stream(None))
+        _exact(out, "out", (T, d), dtype)
+    _run("moe_combine_rows", T, d, k, R, kind, _at(y), _at(inv_row), _at(topk_w), _at(add), _at(out), _stream(None))
     return out
 
 
@@ -856,23 +882,25 @@ def combine_backward(d_out, y, inv_row, topk_w=None, want_dy=True, want_dw=True,
     T, k = _slots(inv_row, "inv_row")
     if y.dim() != 2:
         raise ValueError("y: [R, d] is expected")
-    _here(d_out, y, inv_row, topk_w, dy)
-    (R, d), kind = y.shape, _type(y.dtype, "y")
-    _exact(d_out, "d_out", (T, d), y.dtype)
+    _here(y, d_out, inv_row, topk_w, dy)
+    (R, d), dtype = y.shape, y.dtype
+    kind = _type(dtype, "y")
+    _exact(d_out, "d_out", (T, d), dtype)
     _exact(topk_w, "topk_w", (T, k), torch.float32)
     if dy is not None:
-        _exact(dy, "dy", (R, d), y.dtype)
+        _exact(dy, "dy", (R, d), dtype)
     elif want_dy:
-        dy = torch.empty((R, d), dtype=y.dtype, device=y.device)
+        dy = torch.empty((R, d), dtype=dtype, device=y.device)
     dw = torch.empty((T, k), dtype=torch.float32, device=y.device) if want_dw else None
-    _call("moe_combine_rows_backward", T, d, k, R, kind, _ptr(d_out), _ptr(y), _ptr(inv_row), _ptr(topk_w), _ptr(dy),
-          _ptr(dw), _stream(None))
+    _run("moe_combine_rows_backward", T, d, k, R, kind, _at(d_out), _at(y), _at(inv_row), _at(topk_w), _at(dy), _at(dw),
+         _stream(None))
     return CombineGrads(dy, dw)
 
 
+@functools.lru_cache(maxsize=256)
 def _mx_shapes(shape, weights: bool) -> tuple:
-    """Rows, rows of a weight matrix (0: none) and the shapes of codes and
-    scales of values of this shape."""
+    """Rows, columns, rows of a weight matrix (0: none) and the shapes of codes
+    and scales of values of this shape."""
     if weights and len(shape) != 3:
         raise ValueError(f"weights: {list(shape)}, the call takes [E, N, K]")
     cols = shape[-1]
@@ -881,8 +909,10 @@ def _mx_shapes(shape, weights: bool) -> tuple:
     rows, blocks = 1, cols // MX_BLOCK
     for n in shape[:-1]:
         rows *= n
-    codes = (*shape[:-1], cols // 2)
-    return (rows, shape[1], codes, (shape[0], blocks, shape[1])) if weights else (rows, 0, codes, (*shape[:-1], blocks))
+    codes = torch.Size((*shape[:-1], cols // 2))
+    if weights:
+        return rows, cols, shape[1], codes, torch.Size((shape[0], blocks, shape[1]))
+    return rows, cols, 0, codes, torch.Size((*shape[:-1], blocks))
 
 
 def quantize_mxfp4(x, scale="floor", weights=False, codes=None, scales=None, stream=None):
@@ -891,20 +921,20 @@ def quantize_mxfp4(x, scale="floor", weights=False, codes=None, scales=None, str
     of x [E, N, K], scales [E, K / 32, N] as the products take them."""
     if stream is not None:
         return _on_stream(stream, quantize_mxfp4, x, scale, weights, codes, scales)
-    mx, kind = _mx_scale(scale), _type(x.dtype, "x")
-    rows, matrix, cshape, sshape = _mx_shapes(x.shape, weights)
-    _here(x, codes, scales)
-    m = x if x.dim() == 2 else x.reshape(rows, x.shape[-1])
+    mx, kind, shape, dev = _mx_scale(scale), _type(x.dtype, "x"), x.shape, x.device
+    rows, cols, matrix, cshape, sshape = _mx_shapes(shape, weights)
+    m = x if len(shape) == 2 else x.reshape(rows, cols)
     ld = _rows(m, "x")
+    _here(x, codes, scales)
     if codes is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=x.device)
+        codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
     else:
         _exact(codes, "codes", cshape, torch.uint8)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
     else:
         _exact(scales, "scales", sshape, torch.uint8)
-    _call("moe_quantize_mxfp4", rows, m.shape[1], kind, mx, matrix, _pitched(m), ld, _ptr(codes), _ptr(scales), _stream(None))
+    _run("moe_quantize_mxfp4", rows, cols, kind, mx, matrix, m.data_ptr(), ld, _at(codes), _at(scales), _stream(None))
     return codes, scales
 
 
@@ -912,8 +942,8 @@ def mxfp4_values(codes, scales, dtype=torch.bfloat16, weights=False, out=None, s
     """moe_mxfp4_values: what quantize_mxfp4's codes and scales stand for."""
     if stream is not None:
         return _on_stream(stream, mxfp4_values, codes, scales, dtype, weights, out)
-    shape = (*codes.shape[:-1], 2 * codes.shape[-1])
-    rows, matrix, cshape, sshape = _mx_shapes(shape, weights)
+    shape = torch.Size((*codes.shape[:-1], 2 * codes.shape[-1]))
+    rows, cols, matrix, cshape, sshape = _mx_shapes(shape, weights)
     _here(codes, scales, out)
     kind = _type(dtype if out is None else out.dtype, "out")
     _exact(codes, "codes", cshape, torch.uint8)
@@ -922,7 +952,7 @@ def mxfp4_values(codes, scales, dtype=torch.bfloat16, weights=False, out=None, s
         out = torch.empty(shape, dtype=dtype, device=codes.device)
     else:
         _exact(out, "out", shape, out.dtype)
-    _call("moe_mxfp4_values", rows, shape[-1], kind, matrix, _ptr(codes), _ptr(scales), _ptr(out), _stream(None))
+    _run("moe_mxfp4_values", rows, cols, kind, matrix, _at(codes), _at(scales), _at(out), _stream(None))
     return out
 
 
@@ -931,17 +961,17 @@ def swiglu_mxfp4(g, u, scale="floor", want_h=False, stream=None) -> MxSwiglu:
     one product's rows)."""
     if stream is not None:
         return _on_stream(stream, swiglu_mxfp4, g, u, scale, want_h)
-    mx, ld = _mx_scale(scale), _rows(g, "g", torch.bfloat16)
-    if _rows(u, "u", torch.bfloat16) != ld or u.shape != g.shape:
+    mx, ld, shape = _mx_scale(scale), _rows(g, "g", torch.bfloat16), g.shape
+    if _rows(u, "u", torch.bfloat16) != ld or u.shape != shape:
         raise ValueError("g and u: two matrices of one shape and row pitch are expected")
     _here(g, u)
-    (R, f), dev = g.shape, g.device
-    if f % MX_BLOCK:
-        raise ValueError(f"g: {f} columns are no multiple of {MX_BLOCK}")
-    codes = torch.empty((R, f // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((R, f // MX_BLOCK), dtype=torch.uint8, device=dev)
-    h = torch.empty((R, f), dtype=torch.bfloat16, device=dev) if want_h else None
-    _call("moe_swiglu_mxfp4", R, f, mx, _pitched(g), _pitched(u), ld, _ptr(codes), _ptr(scales), _ptr(h), _stream(None))
+    R, f, _, cshape, sshape = _mx_shapes(shape, False)
+    dev = g.device
+    codes = torch.empty(cshape, dtype=torch.uint8, device=dev)
+    scales = torch.empty(sshape, dtype=torch.uint8, device=dev)
+    h = torch.empty(shape, dtype=torch.bfloat16, device=dev) if want_h else None
+    _run("moe_swiglu_mxfp4", R, f, mx, g.data_ptr(), u.data_ptr(), ld, codes.data_ptr(), scales.data_ptr(), _at(h),
+         _stream(None))
     return MxSwiglu(codes, scales, h)
 
 
@@ -951,23 +981,24 @@ def grouped_mxfp4_gemm(a, a_scales, offsets, w, w_scales, out_dtype=torch.bfloat
     N] (out's rows may lie apart)."""
     if stream is not None:
         return _on_stream(stream, grouped_mxfp4_gemm, a, a_scales, offsets, w, w_scales, out_dtype, out)
-    if a.dim() != 2 or w.dim() != 3 or a.shape[1] != w.shape[2]:
-        raise ValueError(f"a: {list(a.shape)} and w: {list(w.shape)}, the call takes [R, K / 2] and [E, N, K / 2]")
+    ashape, wshape, u8 = a.shape, w.shape, torch.uint8
+    if len(ashape) != 2 or len(wshape) != 3 or ashape[1] != wshape[2]:
+        raise ValueError(f"a: {list(ashape)} and w: {list(wshape)}, the call takes [R, K / 2] and [E, N, K / 2]")
     _here(a, a_scales, offsets, w, w_scales, out)
-    (R, half), (E, N, _) = a.shape, w.shape
+    (R, half), (E, N, _) = ashape, wshape
     K = 2 * half
     if K % MX_BLOCK:
         raise ValueError(f"a: {K} columns are no multiple of {MX_BLOCK}")
-    kind = _type(out_dtype if out is None else out.dtype, "out")
-    _exact(a, "a", (R, half), torch.uint8)
-    _exact(a_scales, "a_scales", (R, K // MX_BLOCK), torch.uint8)
+    _exact(a, "a", ashape, u8)
+    _exact(a_scales, "a_scales", (R, K // MX_BLOCK), u8)
     _exact(offsets, "offsets", (E + 1,), torch.int32)
-    _exact(w, "w", (E, N, half), torch.uint8)
-    _exact(w_scales, "w_scales", (E, K // MX_BLOCK, N), torch.uint8)
+    _exact(w, "w", wshape, u8)
+    _exact(w_scales, "w_scales", (E, K // MX_BLOCK, N), u8)
     if out is None:
         out = torch.empty((R, N), dtype=out_dtype, device=a.device)
     elif out.shape != (R, N):
         raise ValueError(f"out: {list(out.shape)}, the call takes {[R, N]}")
-    _call("moe_grouped_mxfp4_gemm", R, K, N, E, kind, _ptr(a), _ptr(a_scales), _ptr(offsets), _ptr(w), _ptr(w_scales),
-          _pitched(out), _rows(out, "out"), _stream(None))
+    kind = _type(out.dtype, "out")
+    _run("moe_grouped_mxfp4_gemm", R, K, N, E, kind, _at(a), _at(a_scales), _at(offsets), _at(w), _at(w_scales),
+         out.data_ptr(), _rows(out, "out"), _stream(None))
     return out

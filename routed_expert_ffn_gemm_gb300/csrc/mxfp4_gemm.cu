@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
   griddep_wait();
   griddep_launch_dependents();
 
-  row_tiles<ROWS>(p, offs, prefix, kThreads);
+  group_tiles<ROWS>(p, offs, prefix, kThreads);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();

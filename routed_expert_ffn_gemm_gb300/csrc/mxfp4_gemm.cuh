@@ -10,7 +10,6 @@ namespace mx_gemm {
 using block_gemm::Place;
 using block_gemm::kBand;
 using block_gemm::kMaxGroups;
-using block_gemm::row_tiles;
 using block_gemm::warp_wait;
 
 constexpr int kStep = 256;             // of the reduction in a stage: rows of 128 bytes, 8 scales each
@@ -34,6 +33,59 @@ struct Maps {
   CUtensorMap ws;    // weights' scales: 8 blocks of 128 channels (256 for a pair)
   CUtensorMap out;   // 32 rows of 64 bytes (a pair's)
 };
+
+// Group ranges, clamped into [0, R] and ordered, and the prefix of their counts
+// of ROWS-row tiles, in shared memory, as block_gemm's row_tiles; a lane takes
+// consecutive groups, so that there is one scan of each kind over the warp (256
+// groups: 0.3 us of a launch instead of 1.4).  The whole CTA calls this and
+// synchronises afterwards.
+template <int ROWS>
+__device__ __forceinline__ void group_tiles(const Params& p, int* offs, int* prefix, int threads) {
+  for (int g = threadIdx.x; g <= p.E; g += threads) {
+    int o = p.offsets[g];
+    if (o < 0 || o > p.R) {
+      set_device_status(p.status, MOE_ERR_DEVICE_BOUNDS);
+      o = o < 0 ? 0 : p.R;
+    }
+    offs[g] = o;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x, each = p.E / 32 + 1;
+  const int g0 = min(lane * each, p.E + 1), g1 = min(g0 + each, p.E + 1);
+  int top = 0;
+  for (int g = g0; g < g1; ++g) top = max(top, offs[g]);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, top, o);
+    if (lane >= o) top = max(top, v);
+  }
+  int run = __shfl_up_sync(0xffffffffu, top, 1);
+  if (lane == 0) run = 0;
+  for (int g = g0; g < g1; ++g) {  // a decreasing offset becomes the largest before it
+    const int o = offs[g];
+    run = max(run, o);
+    if (run != o) {
+      offs[g] = run;
+      set_device_status(p.status, MOE_ERR_DEVICE_BOUNDS);
+    }
+  }
+  __syncwarp();
+  const int e1 = min(g1, p.E);
+  int sum = 0;
+  for (int g = g0; g < e1; ++g) sum += (offs[g + 1] - offs[g] + ROWS - 1) / ROWS;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int at = incl - sum;
+  for (int g = g0; g < g1; ++g) {
+    prefix[g] = at;
+    if (g < p.E) at += (offs[g + 1] - offs[g] + ROWS - 1) / ROWS;
+  }
+}
 
 // 2^32 / n rounded up, n from 2 to kBand.
 static_assert(kBand == 16, "kInverse");

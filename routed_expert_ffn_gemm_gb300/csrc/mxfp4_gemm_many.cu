@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_many_kernel(const Para
   }
   griddep_wait();
   griddep_launch_dependents();
-  row_tiles<256>(p, offs, prefix, kThreads);
+  group_tiles<256>(p, offs, prefix, kThreads);
   ptx::tc_fence_before();
   ptx::cluster_sync();  // (also: the peers' barriers are initialised)
   ptx::tc_fence_after();

@@ -99,11 +99,10 @@ def combine_backward(d_out, y, inv, w):
     dy = torch.full(y.shape, float("nan"), dtype=torch.float64)
     dw = torch.zeros(inv.shape, dtype=torch.float64)
     mag = dw.clone()
-    for t in range(inv.shape[0]):
-        for j in range(inv.shape[1]):
-            r = int(inv[t, j])
-            if r >= 0:
-                dy[r] = d_out[t].double() * (1 if w is None else w[t, j].double())
-                term = d_out[t].double() * y[r].double()
-                dw[t, j], mag[t, j] = term.sum(), term.abs().sum()
+    for j in range(inv.shape[1]):
+        on = inv[:, j] >= 0
+        r, d = inv[on, j].long(), d_out[on].double()
+        dy[r] = d * (1 if w is None else w[on, j, None].double())
+        terms = d * y[r].double()
+        dw[on, j], mag[on, j] = terms.sum(1), terms.abs().sum(1)
     return dy, dw, mag
