@@ -647,7 +647,8 @@ typedef enum moe_mx_scale {
  * Rows of an expert are in assignment order (bit-exact).  Rows from
  * offsets[E] on are left as they are.  d % 8 == 0, else MOE_ERR_UNSUPPORTED.
  * T == 0: counts and offsets are set to zero.
- *   workspace: moe_dispatch_workspace_size() bytes (the same on every device)
+ *   workspace: moe_dispatch_workspace_size() bytes (the same on every device;
+ *              0: may be NULL).  Calls that overlap on the GPU need one each.
  */
 MOE_API moe_status moe_dispatch(int32_t T, int32_t d, int32_t E, int32_t k, int32_t x_dtype, int32_t rows_dtype,
                                 int32_t scale_kind, const void *x, int64_t ld_x, const int32_t *topk_idx,

@@ -280,7 +280,7 @@ moe_status launch(const DispatchArgs& a, cudaStream_t s) {
   if (R <= kSmallRows) {
     constexpr int WARPS = kSmallThreads / 32;
     const size_t smem = sizeof(int) * ((size_t)WARPS * a.E + a.E + 1 + R);
-    if (smem > 48 * 1024)
+    if (smem > 40 * 1024)  // (48 KB, the static part among them, need no asking)
       MOE_TRY_CUDA(cudaFuncSetAttribute(dispatch_small_kernel<M, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)(sizeof(int) * ((size_t)WARPS * 1024 + 1025 + kSmallRows))));
     const int per = M == kNone ? 0 : M == kCopy ? (a.d * (a.f32 ? 4 : 2) / 16 + 31) / 32 : (a.d / kMxBlock + 31) / 32;

@@ -298,7 +298,7 @@ moe_status mxfp4_gemm_launch(const MxGemmArgs& a, cudaStream_t s) {
   p.ld_out = a.ld_out;
   p.status = a.status;
   p.timeout_ns = a.timeout_ns;
-  if (((long long)a.R / 64 + a.E) * p.MT > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  if (((long long)a.R / 64 + a.E) * p.MT > 0x7fff0000ll) return MOE_ERR_UNSUPPORTED;
   Maps maps;
   MOE_TRY(make_tmap_3d(&maps.w, a.w, a.E, a.N, a.K / 2, a.K / 2, 1, 128, 128, 128));
   MOE_TRY(make_tmap_3d(&maps.ws, a.w_scales, a.E, p.KB, a.N, a.N, 1, 8, 128, 0));

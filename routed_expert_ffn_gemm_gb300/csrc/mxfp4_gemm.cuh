@@ -98,7 +98,7 @@ static __constant__ const unsigned kInverse[kBand + 1] = {
 // Where a warp's units are, asked in ascending order: block_gemm's place_of (row
 // tiles of ROWS rows first inside bands of kBand) in some 100 cycles instead of
 // 1200, which every role would spend on every unit (65536 rows on 128 experts of
-// 768 x 2048, three stages a unit: 88 us before, AFTER here).  The expert is
+// 768 x 2048, three stages a unit: 88 us before, 76 here).  The expert is
 // sought from the last one on by all lanes at once, and the one division left is
 // by a number up to kBand.
 template <int ROWS>
@@ -196,7 +196,7 @@ __device__ __forceinline__ void load_row_scales(const Params& p, bool live, long
 // sets are on their way in registers.  The warp that loads must not fence: a
 // proxy fence waits for the loads in flight, which made each stage take the 1100
 // cycles of a load (16384 rows of 8 experts, 4096 -> 28672: 1120 us with loads in
-// front of the fence, 917 with 4-byte asynchronous copies, AFTER here).
+// front of the fence, 917 with 4-byte asynchronous copies, 626 here).
 template <int ROWS, int GROUPS, int STAGES, typename Empty, typename Raw>
 __device__ __forceinline__ bool row_scales(const Params& p, const int* offs, const int* prefix, int u_first, int u_step,
                                            int units, int first, uint8_t* atoms, int stage_bytes, Empty empty_bar,

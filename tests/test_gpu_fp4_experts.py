@@ -189,6 +189,8 @@ DISPATCH = [
     (2100, 128, 8, 32, 0.07),
     (90, 3, 30, 32, 0.1),      # an expert more than once in a token
     (4000, 33, 5, 8, 0.9),
+    (1905, 610, 1, 32, 0.0),   # shared memory just below the 48 KB that need no asking
+    (2041, 602, 1, 32, 0.0),
 ]
 
 
@@ -396,6 +398,13 @@ PRODUCT = [
     ([4500, 70], 0, 0, 128, 304),
     ([2] * 40, 0, 0, 2048, 128),
     ([130, 250, 512], 0, 0, 768, 384),
+    # many rows: ends inside a tile, next to one, at one, short and long reductions
+    ([300, 0, 113, 256, 511], 3, 2, 256, 240),
+    ([256, 129], 0, 0, 96, 480),
+    ([700], 0, 1, 544, 496),
+    ([400, 150], 0, 0, 1280, 256),
+    ([260, 300], 0, 0, 2592, 496),
+    ([1100], 0, 0, 1024, 16),
 ]
 
 
