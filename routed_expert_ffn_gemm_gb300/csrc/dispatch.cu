@@ -94,32 +94,50 @@ __device__ __forceinline__ int pieces_of(const DispatchArgs& p) {
   return M == kCopy ? (p.d * (p.f32 ? 4 : 2) / 16 + 31) / 32 : (p.d / kMxBlock + 31) / 32;
 }
 
-// One warp: piece `c` of token t to the rows in `rows` (k of them, -1: none).
-template <Move M, bool WIDE>
-__device__ __forceinline__ void move_piece(const DispatchArgs& p, int t, int c, const int* rows) {
-  const int at = c * 32 + (threadIdx.x & 31);
+// One warp: pieces c .. c + N - 1 (those below `pieces`) of token t to the rows in
+// `rows` (k of them, -1: none): all of them are read, then written a row at a
+// time, so that a row gets N x 512 bytes in a go.
+template <Move M, bool WIDE, int N>
+__device__ __forceinline__ void move_pieces(const DispatchArgs& p, int t, int c, const int* rows) {
+  const int lane = threadIdx.x & 31;
   if constexpr (M == kCopy) {
     const int vecs = p.d * (p.f32 ? 4 : 2) / 16;
-    if (at >= vecs) return;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) +
-                                                         (size_t)t * p.ldx * (p.f32 ? 4 : 2)) + at);
-    for (int j = 0; j < p.k; ++j)
-      if (rows[j] >= 0) static_cast<uint4*>(p.rows)[(size_t)rows[j] * vecs + at] = v;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + (size_t)t * p.ldx * (p.f32 ? 4 : 2));
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((c + i) * 32 + lane < vecs) v[i] = __ldg(x + (c + i) * 32 + lane);
+    for (int j = 0; j < p.k; ++j) {
+      if (rows[j] < 0) continue;
+      uint4* to = static_cast<uint4*>(p.rows) + (size_t)rows[j] * vecs + c * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((c + i) * 32 + lane < vecs) to[i * 32] = v[i];
+    }
   } else {
     constexpr bool F32 = M == kMxF32;
     const int nb = p.d / kMxBlock;
-    if (at >= nb) return;
-    MxBlock<F32> b;
-    load_words<MxBlock<F32>::WORDS, WIDE>(
-        static_cast<const uint8_t*>(p.x) + ((size_t)t * p.ldx + (size_t)at * kMxBlock) * (F32 ? 4 : 2), b.w);
-    uint4 codes;
-    const uint32_t s = b.codes(p.fit, codes);
-    for (int j = 0; j < p.k; ++j)
-      if (rows[j] >= 0) {
-        const size_t to = (size_t)rows[j] * nb + at;
-        static_cast<uint4*>(p.rows)[to] = codes;
-        p.row_scales[to] = (uint8_t)s;
-      }
+    uint4 codes[N];
+    uint32_t scale[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (c + i) * 32 + lane;
+      if (at >= nb) continue;
+      MxBlock<F32> b;
+      load_words<MxBlock<F32>::WORDS, WIDE>(
+          static_cast<const uint8_t*>(p.x) + ((size_t)t * p.ldx + (size_t)at * kMxBlock) * (F32 ? 4 : 2), b.w);
+      scale[i] = b.codes(p.fit, codes[i]);
+    }
+    for (int j = 0; j < p.k; ++j) {
+      if (rows[j] < 0) continue;
+      const size_t to = (size_t)rows[j] * nb + c * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((c + i) * 32 + lane < nb) {
+          static_cast<uint4*>(p.rows)[to + i * 32] = codes[i];
+          p.row_scales[to + i * 32] = (uint8_t)scale[i];
+        }
+    }
   }
 }
 
@@ -180,7 +198,7 @@ __global__ void __launch_bounds__(kSmallThreads) dispatch_small_kernel(const Dis
     for (long long i = blockIdx.x + (long long)gridDim.x * warp; i < (long long)p.T * pieces;
          i += (long long)gridDim.x * WARPS) {
       const int t = (int)(i / pieces);
-      move_piece<M, WIDE>(p, t, (int)(i - (long long)t * pieces), row_of + t * p.k);
+      move_pieces<M, WIDE, 1>(p, t, (int)(i - (long long)t * pieces), row_of + t * p.k);
     }
   }
 }
@@ -202,25 +220,48 @@ __global__ void __launch_bounds__(kThreads) dispatch_count_kernel(const Dispatch
 }
 
 // Each chunk's counts become the sums over the chunks before it; counts[e] the
-// total.  A CTA takes 32 experts (the lanes), a warp a slice of the chunks.
+// total.  A CTA takes 32 experts (the lanes), a warp a slice of the chunks, of
+// which the first kHeld stay in registers between the two passes.
 __global__ void __launch_bounds__(1024) dispatch_scan_kernel(int n_chunks, int E, int32_t* __restrict__ chunks,
                                                              int32_t* __restrict__ counts) {
   griddep_begin();
+  constexpr int kHeld = 16;
   __shared__ int part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
   const int per = (n_chunks + 31) / 32, c0 = min(n_chunks, warp * per), c1 = min(n_chunks, c0 + per);
-  int sum = 0;
+  int32_t* at = chunks + (size_t)c0 * E + e;
+  int held[kHeld], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = e < E && c0 + i < c1 ? at[(size_t)i * E] : 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) sum += held[i];
   if (e < E)
 #pragma unroll 8
-    for (int c = c0; c < c1; ++c) sum += chunks[(size_t)c * E + e];
+    for (int c = c0 + kHeld; c < c1; ++c) sum += chunks[(size_t)c * E + e];
   part[warp][lane] = sum;
   __syncthreads();
-  int run = 0;
-  for (int w = 0; w < warp; ++w) run += part[w][lane];
+  {  // warp: expert `warp` of the 32, lane: slice
+    const int v = part[lane][warp];
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    part[lane][warp] = incl - v;
+    if (lane == 31 && blockIdx.x * 32 + warp < E) counts[blockIdx.x * 32 + warp] = incl;
+  }
+  __syncthreads();
   if (e >= E) return;
-  if (warp == 31) counts[e] = run + sum;
+  int run = part[warp][lane];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (c0 + i < c1) {
+      at[(size_t)i * E] = run;
+      run += held[i];
+    }
 #pragma unroll 8
-  for (int c = c0; c < c1; ++c) {
+  for (int c = c0 + kHeld; c < c1; ++c) {
     const int v = chunks[(size_t)c * E + e];
     chunks[(size_t)c * E + e] = run;
     run += v;
@@ -268,9 +309,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchA
   if constexpr (M != kNone) {
     __syncthreads();
     const int pieces = pieces_of<M>(p), tokens = n / p.k, t0 = first / p.k;
+    constexpr int N = M == kCopy ? 8 : 4;  // pieces of a token that a warp holds
     for (int t = blockIdx.y * WARPS + warp; t < tokens; t += gridDim.y * WARPS)
-#pragma unroll 4
-      for (int c = 0; c < pieces; ++c) move_piece<M, WIDE>(p, t0 + t, c, row_of + t * p.k);
+      for (int c = 0; c < pieces; c += N) move_pieces<M, WIDE, N>(p, t0 + t, c, row_of + t * p.k);
   }
 }
 
@@ -295,7 +336,7 @@ moe_status launch(const DispatchArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(int) * ((size_t)(kThreads / 32) * a.E + a.E + 1 + kChunkRows);
   // chunks of few CTAs an SM end unevenly: several CTAs rank a chunk then, and
   // each moves its share of the tokens
-  const int shares = M == kNone ? 1 : min(4, max(1, 16 * a.num_sms / n));
+  const int shares = M == kNone ? 1 : min(8, max(1, 16 * a.num_sms / n));
   MOE_TRY_CUDA(launch_k(dispatch_move_kernel<M, WIDE>, dim3(n, shares), dim3(kThreads), smem, s, a, chunk));
   return MOE_OK;
 }

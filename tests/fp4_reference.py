@@ -66,19 +66,16 @@ def product(a, a_scales, offsets, w, w_scales):
 
 def maps(idx, E):
     """offsets, counts, row_token, inv_row by walking the experts."""
-    flat = idx.reshape(-1).tolist()
-    k = idx.shape[1]
-    inv, token, counts = [-1] * len(flat), [], []
-    for e in range(E):
-        mine = [a for a, x in enumerate(flat) if x == e]
-        for a in mine:
-            inv[a] = len(token)
-            token.append(a // k)
-        counts.append(len(mine))
-    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
-    token += [-1] * (len(flat) - len(token))
-    return (offsets, torch.tensor(counts, dtype=torch.int32), torch.tensor(token, dtype=torch.int32),
-            torch.tensor(inv, dtype=torch.int32).view(idx.shape))
+    flat, k = idx.reshape(-1), idx.shape[1]
+    mine = [torch.nonzero(flat == e)[:, 0] for e in range(E)]
+    counts = torch.tensor([m.numel() for m in mine], dtype=torch.int32)
+    order = torch.cat(mine)
+    inv = torch.full((flat.numel(),), -1, dtype=torch.int32)
+    inv[order] = torch.arange(order.numel(), dtype=torch.int32)
+    token = torch.full((flat.numel(),), -1, dtype=torch.int32)
+    token[: order.numel()] = (order // k).to(torch.int32)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)]).to(torch.int32)
+    return offsets, counts, token, inv.view(idx.shape)
 
 
 def combine(y, inv, w=None, add=None):

@@ -189,6 +189,7 @@ DISPATCH = [
     (2100, 128, 8, 32, 0.07),
     (90, 3, 30, 32, 0.1),      # an expert more than once in a token
     (4000, 33, 5, 8, 0.9),
+    (70000, 40, 2, 8, 0.05),   # slices of more chunks than registers hold
     (1905, 610, 1, 32, 0.0),   # shared memory just below the 48 KB that need no asking
     (2041, 602, 1, 32, 0.0),
 ]
