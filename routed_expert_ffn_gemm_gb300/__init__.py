@@ -1,5 +1,6 @@
 """GB300-native forward of one Mixture-of-Experts FFN layer, and the operators
-that train its routed experts in 8 bits.
+that train its routed experts in 8 bits, run them in 4 bits and move tokens to
+them and back with gradients.
 
 The compute path is a C-ABI CUDA library (``libmoe_gb300.so``, kernels for
 sm_103a) reached through the thin ctypes binding in ``api``.  Importing this

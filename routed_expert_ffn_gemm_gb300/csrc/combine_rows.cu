@@ -4,11 +4,14 @@
 //   dy[inv[t,j],:] = w[t,j] dout[t,:],   dw[t,j] = <dout[t,:], y[inv[t,j],:]>
 //
 // Token by token, so that dout is read once for its k rows and nothing is
-// added atomically.  Forward: a warp takes a piece of 32 x 16 bytes of a token
-// and has the loads of eight rows in flight.  Backward: a CTA takes a token,
-// each thread 16 bytes of dout and of eight rows at a time; eight dot products
-// stay in registers and are summed over lanes, then warps.  Both are bound by
-// memory.
+// added atomically.  A warp takes a token (forward: a token's pieces go to
+// several warps, backward: a CTA takes it, where tokens are few) and keeps eight
+// to twelve loads of 16 bytes in flight a lane: up to eight rows, or several
+// pieces of fewer; the dot products of the weights' gradient stay in registers
+// and are summed over lanes, then warps.  Bound by memory: 16384 tokens of 4096
+// in bf16 with two rows each 77 us forward and 99 backward (floors 79 and 99),
+// 16384 of 2048 with eight 102 and 180 (92 and 169); 64 tokens of 7168 with eight
+// rows 3.4 us forward.
 #include "mxfp4.cuh"
 
 namespace moe {

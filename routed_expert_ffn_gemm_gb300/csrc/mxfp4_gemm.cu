@@ -9,6 +9,12 @@
 // that the tensor cores take, warp 2 turns the weights' scales into atoms,
 // warp 1 copies atoms to tensor memory and issues the MMAs, warps 4..7 hold a
 // quarter of the channels each and write results.  Two accumulators, one filling while the other is written.
+//
+// With few rows the weights are all that moves, and the ring keeps 136 KB of them
+// on their way: 512 rows on 256 experts of 2048 -> 7168 288 us (7.0 TB/s, a copy
+// has 6.8), one row on each of 8 experts of 7168 -> 4096 25 us (5.0 TB/s with
+// launch, prologue and pipeline fill, and 256 units on 152 SMs).  The MMAs would
+// take a tenth of that.
 #include "mxfp4_gemm.cuh"
 
 namespace moe {

@@ -11,6 +11,16 @@
 // Roles of each CTA: warp 0 copies codes and the weights' scales, warp 3 the rows'
 // scales, warp 2 turns the weights' into atoms, warps 4..11 write results (a quarter of the rows, half of the
 // channels each); warp 1 of the even CTA issues the MMAs.
+//
+// What bounds it is shared memory: a stage of 256 is 512 cycles of MMAs, while
+// copies write 37 KB and MMAs and scale copies read 35 KB, 560 cycles at 128
+// bytes a cycle; it takes 620 to 670 (16384 rows on 8 experts of 4096 -> 28672:
+// 585 us in bursts, 6.6 PFLOP/s, tensor pipe 73 % busy; 666 under the power cap).
+// The shared columns cost some 1000 cycles from a unit's last MMA to the next
+// one's first.  With few stages a unit the writing warps set the pace: 3300 of
+// 3900 cycles of a unit of three (65536 rows on 128 experts of 768 -> 2048: 76
+// us).  Results leave by TMA in rows of 64 bytes: 32-byte stores from registers
+// took 132 us there, whole lines by plain stores 110 (as shared memory is busy).
 #include "mxfp4_gemm.cuh"
 
 namespace moe {
