@@ -667,7 +667,8 @@ MOE_API moe_status moe_dispatch_workspace_size(int32_t T, int32_t E, int32_t k, 
  * rounded once to dtype.
  *   rows     [R, d] MOE_BF16 or MOE_F32     inv_row [T, k] int32
  *   topk_w   [T, k] fp32, or NULL: weights of 1 (d_x of moe_dispatch from the
- *            rows' gradients; add: what reaches x another way)
+ *            rows' gradients, MXFP4's rounding passed through; add: what
+ *            reaches x another way)
  *   add      [T, d] dtype or NULL           out [T, d] dtype (may be add)
  * inv_row values from R on are skipped and flag MOE_ERR_DEVICE_BOUNDS.
  * d % 8 == 0, else MOE_ERR_UNSUPPORTED.  T == 0: nothing is enqueued.
@@ -707,7 +708,7 @@ MOE_API moe_status moe_combine_rows_backward(int32_t T, int32_t d, int32_t k, in
  *   codes   [rows, cols/2] out
  *   scales  matrix_rows == 0: [rows, cols/32] out; else x is rows/matrix_rows
  *           weight matrices of matrix_rows rows, scales
- *           [rows/matrix_rows, cols/32, matrix_rows] out (matrix_rows % 16 == 0)
+ *           [rows/matrix_rows, cols/32, matrix_rows] out
  * cols % 32 == 0, else MOE_ERR_UNSUPPORTED.  rows == 0: nothing is enqueued.
  */
 MOE_API moe_status moe_quantize_mxfp4(int32_t rows, int32_t cols, int32_t x_dtype, int32_t scale_kind,
@@ -741,7 +742,8 @@ MOE_API moe_status moe_swiglu_mxfp4(int32_t R, int32_t ffn, int32_t scale_kind, 
  *   out[r,n] = sum_b 2^(sa[r,b] - 127) * 2^(sw[e,b,n] - 127) *
  *              sum_{i in block b} a[r,i] * w[e,n,i]
  *
- * products exact, sums in fp32 on the tensor cores, rounded once to out_dtype.
+ * products exact, sums in fp32 on the tensor cores (a partial sum past its range
+ * makes the result infinite), rounded once to out_dtype.
  *   a_codes [R, K/2]      a_scales [R, K/32]
  *   w_codes [E, N, K/2]   w_scales [E, K/32, N]
  *   out     [R, N] MOE_BF16 or MOE_F32, row pitch ld_out elements

@@ -25,10 +25,7 @@ moe_status check_tokens(int32_t T, int32_t d, int32_t k) {
 moe_status check_mx_rows(int32_t rows, int32_t cols, int32_t dtype, int32_t matrix_rows) {
   if (rows < 0 || matrix_rows < 0) return MOE_ERR_INVALID_ARG;
   if (cols <= 0 || cols % kMxBlock != 0 || rows > kMaxRows || !plain_type(dtype)) return MOE_ERR_UNSUPPORTED;
-  if (matrix_rows > 0) {
-    if (rows % matrix_rows != 0) return MOE_ERR_INVALID_ARG;
-    if (matrix_rows % 16 != 0) return MOE_ERR_UNSUPPORTED;
-  }
+  if (matrix_rows > 0 && rows % matrix_rows != 0) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 

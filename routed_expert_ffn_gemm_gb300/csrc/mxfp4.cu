@@ -68,10 +68,17 @@ __global__ void __launch_bounds__(kThreads) quantize_weights_kernel(const uint8_
       codes[row * nb + kb] = c;
     }
     __syncthreads();
-    const uint32_t k = threadIdx.x >> 3, r = (threadIdx.x & 7u) * 4u;  // (N % 16 == 0: four rows or none)
-    if (o.kb0 + k < nb && o.n0 + r < N)
-      *reinterpret_cast<uint32_t*>(scales + ((size_t)o.m * nb + o.kb0 + k) * N + o.n0 + r) =
-          *reinterpret_cast<const uint32_t*>(&sc[k][r]);
+    const uint32_t k = threadIdx.x >> 3, r = (threadIdx.x & 7u) * 4u;  // four rows of a block
+    if (o.kb0 + k < nb) {
+      uint8_t* to = scales + ((size_t)o.m * nb + o.kb0 + k) * N + o.n0 + r;
+      if ((N & 3u) == 0u) {
+        if (o.n0 + r < N) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(&sc[k][r]);
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+          if (o.n0 + r + i < N) to[i] = sc[k][r + i];
+      }
+    }
     __syncthreads();
   }
 }
@@ -122,9 +129,16 @@ __global__ void __launch_bounds__(kThreads) weight_values_kernel(const uint4* __
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const Tile o = tile_of(t, tiles_n, tiles_k);
     const uint32_t k = threadIdx.x >> 3, r = (threadIdx.x & 7u) * 4u;
-    if (o.kb0 + k < nb && o.n0 + r < N)
-      *reinterpret_cast<uint32_t*>(&sc[k][r]) =
-          *reinterpret_cast<const uint32_t*>(scales + ((size_t)o.m * nb + o.kb0 + k) * N + o.n0 + r);
+    if (o.kb0 + k < nb) {
+      const uint8_t* from = scales + ((size_t)o.m * nb + o.kb0 + k) * N + o.n0 + r;
+      if ((N & 3u) == 0u) {
+        if (o.n0 + r < N) *reinterpret_cast<uint32_t*>(&sc[k][r]) = *reinterpret_cast<const uint32_t*>(from);
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+          if (o.n0 + r + i < N) sc[k][r + i] = from[i];
+      }
+    }
     __syncthreads();
     const uint32_t kb = o.kb0 + lane;
 #pragma unroll

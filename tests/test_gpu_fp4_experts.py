@@ -62,7 +62,8 @@ def test_quantize_rows_bit_exact(rows, cols, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("E,N,K", [(1, 16, 32), (3, 48, 1056), (2, 80, 2080), (1, 304, 64)])
+@pytest.mark.parametrize("E,N,K", [(1, 16, 32), (3, 48, 1056), (2, 80, 2080), (1, 304, 64), (1, 1, 32), (3, 17, 96), (2, 33, 1088),
+                                   (5, 30, 64), (2, 100, 32)])
 def test_quantize_weights_bit_exact(E, N, K, dtype):
     x = normal(E, N, K, seed=N + K, dtype=TYPES[dtype])
     codes, scales = Guarded((E, N, K // 2), torch.uint8, DEV), Guarded((E, K // 32, N), torch.uint8, DEV)
