@@ -232,9 +232,13 @@ moe_status launch_backward(const CombineRowsGradArgs& a, cudaStream_t s) {
   constexpr int ALL = kGradThreads / 32;
   const bool wide = a.T < kTokenWarps * a.num_sms;  // few tokens: a CTA each
   const int ctas = wide ? a.T : ceil_div(a.T, ALL), most = 64 * a.num_sms;
-  auto kern = a.k <= 2 ? (wide ? combine_rows_backward_kernel<F32, DROWS, DW, 2, 4, ALL> : combine_rows_backward_kernel<F32, DROWS, DW, 2, 4, 1>)
-              : a.k <= 4 ? (wide ? combine_rows_backward_kernel<F32, DROWS, DW, 4, 2, ALL> : combine_rows_backward_kernel<F32, DROWS, DW, 4, 2, 1>)
-                         : (wide ? combine_rows_backward_kernel<F32, DROWS, DW, 8, 1, ALL> : combine_rows_backward_kernel<F32, DROWS, DW, 8, 1, 1>);
+  auto few = a.k <= 2   ? combine_rows_backward_kernel<F32, DROWS, DW, 2, 4, ALL>
+             : a.k <= 4 ? combine_rows_backward_kernel<F32, DROWS, DW, 4, 2, ALL>
+                        : combine_rows_backward_kernel<F32, DROWS, DW, 8, 1, ALL>;
+  auto many = a.k <= 2   ? combine_rows_backward_kernel<F32, DROWS, DW, 2, 4, 1>
+              : a.k <= 4 ? combine_rows_backward_kernel<F32, DROWS, DW, 4, 2, 1>
+                         : combine_rows_backward_kernel<F32, DROWS, DW, 8, 1, 1>;
+  auto kern = wide ? few : many;
   MOE_TRY_CUDA(launch_k(kern, dim3(ctas < most ? ctas : most), dim3(kGradThreads), 0, s, a));
   return MOE_OK;
 }
@@ -273,9 +277,9 @@ moe_status combine_rows_launch(const CombineRowsArgs& a, cudaStream_t s) {
 moe_status combine_rows_backward_launch(const CombineRowsGradArgs& a, cudaStream_t s) {
   const bool dr = a.d_rows != nullptr, dw = a.dw != nullptr;
   if (!dr && !dw) return MOE_OK;
-  if (a.f32)
-    return !dr ? launch_backward<true, false, true>(a, s) : dw ? launch_backward<true, true, true>(a, s) : launch_backward<true, true, false>(a, s);
-  return !dr ? launch_backward<false, false, true>(a, s) : dw ? launch_backward<false, true, true>(a, s) : launch_backward<false, true, false>(a, s);
+  if (!dr) return a.f32 ? launch_backward<true, false, true>(a, s) : launch_backward<false, false, true>(a, s);
+  if (!dw) return a.f32 ? launch_backward<true, true, false>(a, s) : launch_backward<false, true, false>(a, s);
+  return a.f32 ? launch_backward<true, true, true>(a, s) : launch_backward<false, true, true>(a, s);
 }
 
 }  // namespace moe

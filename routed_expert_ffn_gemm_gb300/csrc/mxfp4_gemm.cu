@@ -8,7 +8,8 @@
 // reduction a stage), warp 3 brings the rows' scales into the 512-byte atoms
 // that the tensor cores take, warp 2 turns the weights' scales into atoms,
 // warp 1 copies atoms to tensor memory and issues the MMAs, warps 4..7 hold a
-// quarter of the channels each and write results.  Two accumulators, one filling while the other is written.
+// quarter of the channels each and write results.  Two accumulators, one filling
+// while the other is written.
 //
 // With few rows the weights are all that moves, and the ring keeps 136 KB of them
 // on their way: 512 rows on 256 experts of 2048 -> 7168 288 us (7.0 TB/s, a copy
@@ -113,7 +114,9 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(const Params p,
     bool ok = true;
     for (int u = u_first; u < units && ok; u += u_step) {
       const Place x = places.at(u);
-      int box = 0;  // the box holds the rows; what the MMA reads past it is any earlier stage's, in columns that nobody stores
+      // the box holds the rows; what the MMA reads past it is any earlier stage's, in
+      // columns that nobody stores
+      int box = 0;
       while (box < T::BOXES - 1 && x.n_valid > 8 << box) ++box;
       const uint32_t bytes = kWeightBytes + (8u << box) * 128u;
       const uint64_t pol = x.tiles > 1 ? keep : once;

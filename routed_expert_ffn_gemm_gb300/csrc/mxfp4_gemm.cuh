@@ -105,7 +105,8 @@ template <int ROWS>
 struct Units {
   const int *offs, *prefix;
   int E, MT, g;
-  __device__ __forceinline__ Units(const Params& p, const int* o, const int* pre) : offs(o), prefix(pre), E(p.E), MT(p.MT), g(0) {}
+  __device__ __forceinline__ Units(const Params& p, const int* o, const int* pre)
+      : offs(o), prefix(pre), E(p.E), MT(p.MT), g(0) {}
 
   // (the whole warp)
   __device__ __forceinline__ Place at(int u) {

@@ -8,9 +8,10 @@
 // there are, so the accumulators share 24 columns: the warps that hold them
 // read them first, and the next unit's MMAs start behind that.
 //
-// Roles of each CTA: warp 0 copies codes and the weights' scales, warp 3 the rows'
-// scales, warp 2 turns the weights' into atoms, warps 4..11 write results (a quarter of the rows, half of the
-// channels each); warp 1 of the even CTA issues the MMAs.
+// Roles of each CTA: warp 0 copies codes and the weights' scales, warp 3 brings the
+// rows' scales, warp 2 turns the weights' into atoms, warps 4..11 write results (a
+// quarter of the rows, half of the channels each); warp 1 of the even CTA issues
+// the MMAs.  (A second warp for the atoms changed nothing.)
 //
 // What bounds it is shared memory: a stage of 256 is 512 cycles of MMAs, while
 // copies write 37 KB and MMAs and scale copies read 35 KB, 560 cycles at 128
@@ -30,7 +31,7 @@ using namespace mx_gemm;
 using block_gemm::kOutBytes;
 
 constexpr int kThreads = 384;
-constexpr int kTileBytes = 128 * 128;
+constexpr int kTileBytes = 128 * 128;  // 128 rows or channels of 256 codes
 constexpr int kStages = 5, kStageBytes = 2 * kTileBytes;
 constexpr int kAtoms = 6;             // of a stage: rows 2, weights 2 of each 128 channels
 constexpr int kEpiWarps = 8, kOutBufs = 2;

@@ -293,7 +293,9 @@ def test_combine(T, k, d, more, drop, dtype):
         if wi is None:
             assert torch.equal(api.dispatch_backward(args[0], args[1], args[3]), out.t)
     dest = add.to(DEV)
-    assert torch.equal(api.combine(y.to(DEV), inv.to(DEV), w.to(DEV), dest, out=dest), api.combine(y.to(DEV), inv.to(DEV), w.to(DEV), add.to(DEV)))
+    on = [v.to(DEV) for v in (y, inv, w)]
+    want = api.combine(*on, add.to(DEV))
+    assert torch.equal(api.combine(*on, dest, out=dest), want)
 
 
 @pytest.mark.parametrize("T,k,d,more,drop", COMBINE)
