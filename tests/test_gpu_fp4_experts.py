@@ -463,13 +463,30 @@ def test_product_keeps_nan_to_its_rows_and_channels(count):
     near(got[~nan], y[~nan], mag[~nan], 320, torch.bfloat16)
 
 
-def test_product_clamps_offsets_out_of_range():
-    R, a, sa, off, w, sw = product_case([4, 4, 4], 0, 0, 64, 32)
-    bad = torch.tensor([-3, 4, 2, 40], dtype=torch.int32)
-    got = api.grouped_mxfp4_gemm(*(v.to(DEV) for v in (a, sa, bad, w, sw)), out_dtype=torch.float32)
+@pytest.mark.parametrize("R,bad,good", [(12, [-3, 4, 2, 40], [0, 4, 4, 12]), (500, [-9, 300, 200, 5000], [0, 300, 300, 500]),
+                                        (150, [0, 90, 2 ** 31 - 1, -2 ** 31], [0, 90, 150, 150])])
+def test_product_clamps_offsets_out_of_range(R, bad, good):
+    _, a, sa, _, w, sw = product_case([R, 0, 0], 0, 0, 64, 32)
+    got = api.grouped_mxfp4_gemm(*(v.to(DEV) for v in (a, sa, torch.tensor(bad, dtype=torch.int32), w, sw)), out_dtype=torch.float32)
     assert api.moe_read_device_status() == api.ERR_DEVICE_BOUNDS
-    y, mag = ref.product(a, sa, torch.tensor([0, 4, 4, 12], dtype=torch.int32), w, sw)
+    y, mag = ref.product(a, sa, torch.tensor(good, dtype=torch.int32), w, sw)
     near(got.cpu(), y, mag, 64, torch.float32)
+
+
+@pytest.mark.parametrize("E,rows,empty", [(1024, 3, 0.7), (1000, 120, 0.6), (1024, 600, 0.5), (333, 400, 0.1)])
+def test_product_many_experts(E, rows, empty):
+    # (few, some and many rows an expert on average; long stretches without any)
+    g = gen(E + rows)
+    counts = torch.randint(1, 2 * rows, (E,), generator=g)
+    counts[torch.rand(E, generator=g) < empty] = 0
+    counts[E // 3:E // 3 + 70] = 0
+    off = offsets_of(counts.tolist())
+    R, K, N = int(off[-1]), 64, 48
+    a, sa = api.quantize_mxfp4(normal(R, K, seed=1).to(DEV))
+    w, sw = api.quantize_mxfp4(normal(E, N, K, seed=2).to(DEV), weights=True)
+    got = api.grouped_mxfp4_gemm(a, sa, off.to(DEV), w, sw).cpu()
+    y, mag = ref.product(a.cpu(), sa.cpu(), off, w.cpu(), sw.cpu())
+    near(got, y, mag, K, torch.bfloat16)
 
 
 def test_product_without_rows():
