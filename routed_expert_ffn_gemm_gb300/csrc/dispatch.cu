@@ -90,11 +90,14 @@ __device__ __forceinline__ void expert_bases(const int* tot, int* base, int E, i
   __syncthreads();
 }
 
+// 16-byte vectors of a row (its bytes may pass 2^31).
+__host__ __device__ __forceinline__ int vecs_of(const DispatchArgs& p) { return p.d / (p.f32 ? 4 : 8); }
+
 // Pieces of a token's row that a warp moves at a time: 32 lanes of 16 bytes
 // (kCopy) or of a block of 32 columns.
 template <Move M>
-__device__ __forceinline__ int pieces_of(const DispatchArgs& p) {
-  return M == kCopy ? (p.d * (p.f32 ? 4 : 2) / 16 + 31) / 32 : (p.d / kMxBlock + 31) / 32;
+__host__ __device__ __forceinline__ int pieces_of(const DispatchArgs& p) {
+  return M == kNone ? 0 : ((M == kCopy ? vecs_of(p) : p.d / kMxBlock) + 31) / 32;
 }
 
 // One warp: pieces c .. c + N - 1 (those below `pieces`) of token t to the rows in
@@ -104,7 +107,7 @@ template <Move M, bool WIDE, int N>
 __device__ __forceinline__ void move_pieces(const DispatchArgs& p, int t, int c, const int* rows) {
   const int lane = threadIdx.x & 31;
   if constexpr (M == kCopy) {
-    const int vecs = p.d * (p.f32 ? 4 : 2) / 16;
+    const int vecs = vecs_of(p);
     const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + (size_t)t * p.ldx * (p.f32 ? 4 : 2));
     uint4 v[N];
 #pragma unroll
@@ -329,8 +332,7 @@ moe_status launch(const DispatchArgs& a, cudaStream_t s) {
     if (smem > 40 * 1024)  // (48 KB, the static part among them, need no asking)
       MOE_TRY_CUDA(cudaFuncSetAttribute(dispatch_small_kernel<M, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)(sizeof(int) * ((size_t)WARPS * 1024 + 1025 + kSmallRows))));
-    const int per = M == kNone ? 0 : M == kCopy ? (a.d * (a.f32 ? 4 : 2) / 16 + 31) / 32 : (a.d / kMxBlock + 31) / 32;
-    const long long pieces = (long long)a.T * per;
+    const long long pieces = (long long)a.T * pieces_of<M>(a);
     const int grid = M == kNone ? 1 : (int)(pieces < a.num_sms ? pieces : a.num_sms);
     MOE_TRY_CUDA(launch_k(dispatch_small_kernel<M, WIDE>, dim3(grid), dim3(kSmallThreads), smem, s, a));
     return MOE_OK;
