@@ -26,6 +26,7 @@ constexpr int kSmallRows = 2048;
 constexpr int kSmallThreads = 512;
 constexpr int kChunkRows = 256;  // assignments of a chunk at most (whole tokens)
 constexpr int kThreads = 256;
+constexpr int kMoveWarps = 4;    // items an SM from which on a warp holds several pieces
 
 enum Move { kNone, kCopy, kMxBf16, kMxF32 };
 
@@ -274,8 +275,9 @@ __global__ void __launch_bounds__(1024) dispatch_scan_kernel(int n_chunks, int E
   }
 }
 
-// smem: cnt[8][E], base[E + 1], row_of[kChunkRows]
-template <Move M, bool WIDE>
+// smem: cnt[8][E], base[E + 1], row_of[kChunkRows].  N: pieces of a token that a
+// warp holds at a time.
+template <Move M, bool WIDE, int N>
 __global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchArgs p, int chunk) {
   griddep_begin();
   constexpr int WARPS = kThreads / 32;
@@ -314,12 +316,20 @@ __global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchA
     for (int x = threadIdx.x; x <= E; x += kThreads) p.offsets[x] = base[x];
   if constexpr (M != kNone) {
     __syncthreads();
-    const int pieces = pieces_of<M>(p), tokens = n / p.k, t0 = first / p.k;
-    // pieces of a token that a warp holds (16384 x 2048 to eight rows each: 102 us
-    // with one, 98 with four, 97 with eight; MXFP4 of 4096 x 7168: 43 with two, 40)
-    constexpr int N = M == kCopy ? 8 : 4;
-    for (int t = blockIdx.y * WARPS + warp; t < tokens; t += gridDim.y * WARPS)
-      for (int c = 0; c < pieces; c += N) move_pieces<M, WIDE, N>(p, t0 + t, c, row_of + t * p.k);
+    // (consecutive warps, consecutive N pieces of a token)
+    const int per = (pieces_of<M>(p) + N - 1) / N, tokens = n / p.k, t0 = first / p.k;
+    const int i = blockIdx.y * WARPS + warp, step = gridDim.y * WARPS;
+    int t = i / per, c = i - t * per;
+    const int step_t = step / per, step_c = step - step_t * per;
+    while (t < tokens) {
+      move_pieces<M, WIDE, N>(p, t0 + t, c * N, row_of + t * p.k);
+      t += step_t;
+      c += step_c;
+      if (c >= per) {
+        c -= per;
+        ++t;
+      }
+    }
   }
 }
 
@@ -341,11 +351,26 @@ moe_status launch(const DispatchArgs& a, cudaStream_t s) {
   MOE_TRY_CUDA(launch_k(dispatch_count_kernel, dim3(n), dim3(kThreads), sizeof(int) * a.E, s, a, chunk));
   MOE_TRY_CUDA(launch_k(dispatch_scan_kernel, dim3(ceil_div(a.E, 32)), dim3(1024), 0, s, n, a.E, a.chunks, a.counts));
   const size_t smem = sizeof(int) * ((size_t)(kThreads / 32) * a.E + a.E + 1 + kChunkRows);
-  // few chunks an SM end unevenly: several CTAs rank a chunk then, and each moves
-  // its share of the tokens (512 chunks: 112 us with one, 102 with four; 128
-  // chunks of two assignments a token: 81 with four, 72 with sixteen)
-  const int shares = M == kNone ? 1 : min(8, max(1, 16 * a.num_sms / n));
-  MOE_TRY_CUDA(launch_k(dispatch_move_kernel<M, WIDE>, dim3(n, shares), dim3(kThreads), smem, s, a, chunk));
+  // Pieces of a token that a warp holds: several where that still leaves items for
+  // the SMs (16384 x 2048 to eight rows each: 102 us with one, 98 with four, 97
+  // with eight; MXFP4 of 4096 x 7168: 43 with two, 40 with four; 2049 x 4096 to one
+  // row: 13.7 with one, 9.1 with eight), one where there are few tokens (128 x
+  // 7168 to 32 rows: 16.5 with one, 20.6 with eight; 342 x 2048 to six: 7.8, 9.3).
+  constexpr int WARPS = kThreads / 32, MANY = M == kNone ? 1 : M == kCopy ? 8 : 4;
+  const int pieces = pieces_of<M>(a);
+  const bool many = (long long)a.T * ceil_div(pieces, MANY) >= (long long)kMoveWarps * a.num_sms;
+  // Few chunks an SM end unevenly: up to eight CTAs rank a chunk then, and each
+  // moves its share of what the chunk's tokens have (512 chunks: 112 us with one,
+  // 102 with four; 128 of two assignments a token 81 with four, 68 with eight).
+  // Chunks that leave SMs idle are shared among more, four CTAs an SM (65 tokens of
+  // 7168 to 32 rows, nine chunks: 63 us where a warp took whole tokens, which gave
+  // nine CTAs work, 11.3 here; 257 to eight rows 21 and 10.7; 40 chunks of 512: 9.5
+  // with sixteen each, 8.4 here).
+  const long long items = (long long)(chunk / a.k) * ceil_div(pieces, many ? MANY : 1);
+  const int most = max(max(1, min(8, 16 * a.num_sms / n)), 4 * a.num_sms / n);
+  const int shares = M == kNone ? 1 : (int)max(1ll, min((long long)most, (items + WARPS - 1) / WARPS));
+  auto kern = many ? dispatch_move_kernel<M, WIDE, MANY> : dispatch_move_kernel<M, WIDE, 1>;
+  MOE_TRY_CUDA(launch_k(kern, dim3(n, shares), dim3(kThreads), smem, s, a, chunk));
   return MOE_OK;
 }
 

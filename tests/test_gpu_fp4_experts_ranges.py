@@ -1,10 +1,12 @@
 """The 4-bit operators and the token movement over their ranges: rows past 2^31
-bytes."""
+bytes, dispatch just past the assignments of its one-launch form."""
 
 import pytest
 import torch
 
 from routed_expert_ffn_gemm_gb300 import api, build
+from tests import fp4_reference as ref
+from tests.test_gpu_fp4_experts import normal, routes
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -30,3 +32,63 @@ def test_rows_past_32_bits_of_bytes(d, dtype):
     assert r.inv_row.tolist() == [[1, 0]]
     out = api.combine(r.rows, r.inv_row)
     assert torch.equal(out, x + x)
+
+
+@pytest.mark.parametrize("quantize", [None, "fit"])
+@pytest.mark.parametrize("T,k,E,d,dtype", [
+    (65, 32, 256, 7168, torch.bfloat16), (70, 31, 40, 1056, torch.float32), (257, 8, 256, 7168, torch.bfloat16),
+    (300, 7, 8, 288, torch.bfloat16), (2049, 1, 8, 4096, torch.bfloat16), (1025, 2, 1024, 8224, torch.float32),
+    (2500, 3, 5, 32, torch.bfloat16), (700, 3, 16, 16416, torch.bfloat16), (9000, 8, 64, 544, torch.bfloat16)])
+def test_tokens_shared_among_ctas(T, k, E, d, dtype, quantize):
+    # chunks of few and of many tokens, rows of one piece, of some and of many
+    x, idx = normal(T, d, seed=T, dtype=dtype), routes(T, E, k, 0.1, seed=k)
+    off, counts, token, inv = ref.maps(idx, E)
+    r = api.dispatch(x.to(DEV), idx.to(DEV), E, quantize)
+    n = int(off[-1])
+    assert torch.equal(r.offsets.cpu(), off) and torch.equal(r.counts.cpu(), counts)
+    assert torch.equal(r.row_token.cpu(), token) and torch.equal(r.inv_row.cpu(), inv)
+    if quantize is None:
+        assert torch.equal(r.rows[:n].cpu(), x[token[:n].long()])
+    else:
+        codes, scales = (t.cpu() for t in api.quantize_mxfp4(x.to(DEV), quantize))
+        assert torch.equal(r.rows[:n].cpu(), codes[token[:n].long()])
+        assert torch.equal(r.scales[:n].cpu(), scales[token[:n].long()])
+
+
+def us_of(*calls, n=20, rounds=9):
+    """Median times of the calls on the GPU, each as a graph of n of them, taken in turn."""
+    graphs, times, s = [], [[] for _ in calls], torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for c in calls:
+            c()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                for _ in range(n):
+                    c()
+            g.replay()
+            graphs.append(g)
+        for _ in range(rounds):
+            for g, t in zip(graphs, times):
+                a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                a.record(s)
+                g.replay()
+                b.record(s)
+                b.synchronize()
+                t.append(1000 * a.elapsed_time(b) / n)
+    return [sorted(t)[rounds // 2] for t in times]
+
+
+@pytest.mark.parametrize("T,k,E,d", [(65, 32, 256, 7168), (257, 8, 256, 7168), (2049, 1, 8, 4096)])
+def test_few_long_rows_take_every_sm(T, k, E, d):
+    # the same rows by the layer's own permutation, which gives a warp each: a
+    # dispatch that leaves SMs idle takes a multiple of its time (65 tokens with
+    # 32 rows each on nine CTAs four times), one that takes them all as long
+    x, idx = normal(T, d, seed=1).to(DEV), routes(T, E, k, 0.0, seed=2).to(DEV)
+    p, R = api.problem(T, d, 128, E, k), T * k
+    new = lambda *n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=DEV)  # noqa: E731
+    out, rows, work = [new(n) for n in (E, E + 1, R, R)], new(R, d, dtype=x.dtype), api.workspace_for(p)
+    mine, other = new(api.moe_dispatch_workspace_size(T, E, k), dtype=torch.uint8), new(R, d, dtype=x.dtype)
+    ours, layers = us_of(lambda: api.dispatch(x, idx, E, rows=rows, workspace=mine),
+                         lambda: api.moe_permute(p, idx, x, *out, other, work))
+    assert torch.equal(rows, other)
+    assert ours < 1.5 * layers, (ours, layers)
