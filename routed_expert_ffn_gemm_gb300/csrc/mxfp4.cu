@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) quantize_weights_kernel(const uint8_
                                                                     uint4* __restrict__ codes,
                                                                     uint8_t* __restrict__ scales) {
   griddep_begin();
-  __shared__ uint8_t sc[kTile][kTile + 4];  // [block][row]
+  __shared__ __align__(4) uint8_t sc[kTile][kTile + 4];  // [block][row], read four rows at a time
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t tiles_n = (N + kTile - 1) / kTile, tiles_k = (nb + kTile - 1) / kTile;
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) weight_values_kernel(const uint4* __
                                                                  const uint8_t* __restrict__ scales, uint32_t tiles,
                                                                  uint32_t nb, uint32_t N, uint8_t* __restrict__ out) {
   griddep_begin();
-  __shared__ uint8_t sc[kTile][kTile + 4];
+  __shared__ __align__(4) uint8_t sc[kTile][kTile + 4];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t tiles_n = (N + kTile - 1) / kTile, tiles_k = (nb + kTile - 1) / kTile;
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
