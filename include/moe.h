@@ -742,8 +742,9 @@ MOE_API moe_status moe_swiglu_mxfp4(int32_t R, int32_t ffn, int32_t scale_kind, 
  *   out[r,n] = sum_b 2^(sa[r,b] - 127) * 2^(sw[e,b,n] - 127) *
  *              sum_{i in block b} a[r,i] * w[e,n,i]
  *
- * products exact, sums in fp32 on the tensor cores (a partial sum past its range
- * makes the result infinite), rounded once to out_dtype.
+ * products exact down to 2^-149, fp32's least step (below it each may lose up to
+ * one), sums in fp32 on the tensor cores (a partial sum past its range makes the
+ * result infinite), rounded once to out_dtype.
  *   a_codes [R, K/2]      a_scales [R, K/32]
  *   w_codes [E, N, K/2]   w_scales [E, K/32, N]
  *   out     [R, N] MOE_BF16 or MOE_F32, row pitch ld_out elements

@@ -1,12 +1,13 @@
 """The 4-bit operators and the token movement over their ranges: rows past 2^31
-bytes, dispatch just past the assignments of its one-launch form."""
+bytes, dispatch just past the assignments of its one-launch form, the product
+at the ends of the scales."""
 
 import pytest
 import torch
 
 from routed_expert_ffn_gemm_gb300 import api, build
 from tests import fp4_reference as ref
-from tests.test_gpu_fp4_experts import normal, routes
+from tests.test_gpu_fp4_experts import gen, normal, offsets_of, routes
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -92,3 +93,63 @@ def test_few_long_rows_take_every_sm(T, k, E, d):
                          lambda: api.moe_permute(p, idx, x, *out, other, work))
     assert torch.equal(rows, other)
     assert ours < 1.5 * layers, (ours, layers)
+
+
+# ------------------------------------------------------------------- product
+
+KERNELS = pytest.mark.parametrize("count", [4, 100, 300], ids=["few", "some", "many"])
+STEP = 2.0 ** -149  # fp32's least
+
+
+def codes_of(*shape, seed):
+    return torch.randint(0, 256, shape, generator=gen(seed), dtype=torch.uint8)
+
+
+def scales_of(value, *shape):
+    return torch.full(shape, value, dtype=torch.uint8)
+
+
+def multiply(a, sa, w, sw):
+    on = [t.to(DEV) for t in (a, sa, offsets_of([a.shape[0]]), w, sw)]
+    return api.grouped_mxfp4_gemm(*on, out_dtype=torch.float32).cpu(), ref.product(a, sa, offsets_of([a.shape[0]]), w, sw)[0]
+
+
+@KERNELS
+@pytest.mark.parametrize("sa,sw", [(254, 0), (0, 254), (1, 253), (253, 1), (127, 0), (0, 127), (20, 110), (107, 0), (0, 107), (54, 53)])
+def test_product_scale_ends(count, sa, sw):
+    # products are multiples of 2^(sa + sw - 256), here at least 2^-149, and a sum
+    # of 320 of them is below 2^16 such steps: fp32 holds every partial sum
+    K, N = 320, 160
+    got, want = multiply(codes_of(count, K // 2, seed=sa), scales_of(sa, count, K // 32), codes_of(1, N, K // 2, seed=sw), scales_of(sw, 1, K // 32, N))
+    assert torch.equal(got.double(), want)
+
+
+@KERNELS
+def test_product_every_scale(count):
+    # a block's two scales make 1 together: every byte from 0 to 254 in each place
+    K, N = 32 * 255, 48
+    at = torch.randperm(255, generator=gen(count)).to(torch.uint8)
+    got, want = multiply(codes_of(count, K // 2, seed=1), at.expand(count, -1).contiguous(), codes_of(1, N, K // 2, seed=2),
+                         (254 - at)[None, :, None].expand(-1, -1, N).contiguous())
+    assert torch.equal(got.double(), want)
+
+
+@KERNELS
+def test_product_past_the_largest(count):
+    # one code in a row: the result is that code times 2^127, infinite from 2 on
+    K, N = 96, 32
+    code = torch.zeros(count, K, dtype=torch.uint8)
+    code[torch.arange(count), torch.arange(count) % K] = (torch.arange(count) % 16).to(torch.uint8)
+    got, want = multiply(ref.pack(code), scales_of(254, count, K // 32), scales_of(0x22, 1, N, K // 2), scales_of(127, 1, K // 32, N))
+    assert torch.equal(got, want.float()) and bool(torch.isinf(got).any()) == (count > 4)
+
+
+@KERNELS
+@pytest.mark.parametrize("sa,sw", [(50, 55), (100, 3), (60, 40), (0, 90), (0, 0)])
+def test_product_below_the_least_step(count, sa, sw):
+    # an instruction loses less than a step of each of its 64 products and of
+    # their sum
+    K, N = 320, 160
+    got, want = multiply(codes_of(count, K // 2, seed=sa), scales_of(sa, count, K // 32), codes_of(1, N, K // 2, seed=sw), scales_of(sw, 1, K // 32, N))
+    assert ((got.double() - want).abs() <= 65 * (K // 64) * STEP).all()
+    assert sa + sw > 0 or not got.any()
