@@ -1,6 +1,6 @@
 """The 4-bit operators and the token movement over their ranges: rows past 2^31
 bytes, dispatch just past the assignments of its one-launch form, the product
-at the ends of the scales."""
+at the ends of the scales and on the quantiser's NaN blocks."""
 
 import pytest
 import torch
@@ -153,3 +153,20 @@ def test_product_below_the_least_step(count, sa, sw):
     got, want = multiply(codes_of(count, K // 2, seed=sa), scales_of(sa, count, K // 32), codes_of(1, N, K // 2, seed=sw), scales_of(sw, 1, K // 32, N))
     assert ((got.double() - want).abs() <= 65 * (K // 64) * STEP).all()
     assert sa + sw > 0 or not got.any()
+
+
+@KERNELS
+def test_product_of_values_that_are_not_finite(count):
+    # what the quantiser makes of them: the NaN scale and codes of 0, also where
+    # the other operand has nothing but zeros
+    K, N, E = 320, 160, 2
+    x, w = normal(E * count, K, seed=count), normal(E, N, K, seed=count + 1)
+    x[:, 96:128], w[:, :, 288:] = 0, 0
+    x[1, 40], x[count, 300], w[0, 9, 100], w[1, 77, 5] = float("nan"), float("inf"), float("-inf"), float("nan")
+    a, sa = api.quantize_mxfp4(x.to(DEV))
+    wq, sw = api.quantize_mxfp4(w.to(DEV), weights=True)
+    assert int((sa == 255).sum()) == 2 and not a.cpu()[1, 16:32].any()
+    got = api.grouped_mxfp4_gemm(a, sa, offsets_of([count] * E).to(DEV), wq, sw).cpu()
+    nan = torch.zeros(E * count, N, dtype=torch.bool)
+    nan[1], nan[count], nan[:count, 9], nan[count:, 77] = True, True, True, True
+    assert torch.equal(torch.isnan(got), nan) and torch.isfinite(got[~nan]).all()
