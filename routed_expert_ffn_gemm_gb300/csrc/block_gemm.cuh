@@ -59,8 +59,8 @@ __device__ __forceinline__ Place place_of(int u, const int* offs, const int* pre
 // Group ranges, clamped into [0, R] and ordered, and the prefix of their
 // counts of ROWS-row tiles, in shared memory.  The whole CTA calls this and
 // synchronises afterwards.
-template <int ROWS, typename P>
-__device__ __forceinline__ void row_tiles(const P& p, int* offs, int* prefix, int threads) {
+template <int ROWS>
+__device__ __forceinline__ void row_tiles(const Params& p, int* offs, int* prefix, int threads) {
   const int lane = threadIdx.x & 31;
   for (int g = threadIdx.x; g <= p.E; g += threads) {
     int o = p.offsets[g];
