@@ -918,7 +918,9 @@ def _mx_shapes(shape, weights: bool) -> tuple:
 def quantize_mxfp4(x, scale="floor", weights=False, codes=None, scales=None, stream=None):
     """moe_quantize_mxfp4 of x [..., cols] (a matrix's rows may lie apart):
     (codes uint8 [..., cols / 2], scales uint8 [..., cols / 32]); with weights
-    of x [E, N, K], scales [E, K / 32, N] as the products take them."""
+    of x [E, N, K], scales [E, K / 32, N] as the products take them.  Of a view
+    that is no such matrix, a transposed one for instance, torch makes a copy
+    first."""
     if stream is not None:
         return _on_stream(stream, quantize_mxfp4, x, scale, weights, codes, scales)
     mx, kind, shape, dev = _mx_scale(scale), _type(x.dtype, "x"), x.shape, x.device

@@ -9,9 +9,9 @@
 // to twelve loads of 16 bytes in flight a lane: up to eight rows, or several
 // pieces of fewer; the dot products of the weights' gradient stay in registers
 // and are summed over lanes, then warps.  Bound by memory: 16384 tokens of 4096
-// in bf16 with two rows each 77 us forward and 99 backward (floors 79 and 99),
-// 16384 of 2048 with eight 102 and 180 (92 and 169); 64 tokens of 7168 with eight
-// rows 3.4 us forward.
+// in bf16 with two rows each 77 us forward and 99 backward (79 and 99 at the rate
+// of a copy), 16384 of 2048 with eight 108 and 180 (99 and 169); 64 tokens of 7168
+// with eight rows 3.4 us forward.
 #include "mxfp4.cuh"
 
 namespace moe {
@@ -19,9 +19,16 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kGradThreads = 128;
-constexpr int kItems = 64;         // forward: warps an SM for which a token's columns are shared out
+// Forward: warps an SM for which a token's columns are shared out (2048 tokens of
+// 7168 with eight rows each: 58 us with 16, 62 with 32, 54 with 64, 51 with 128, 52
+// with 256; 2048 of 4096 with two 8.8 with 16, 7.3 with each of the others).
+constexpr int kItems = 64;
 constexpr long long kMaxGrid = 1 << 20;
-constexpr int kTokenWarps = 16;  // backward: from this many tokens an SM on a warp takes a token, below a CTA
+// Backward: from this many tokens an SM on a warp takes a token, below a CTA.  A
+// warp and a CTA each: 2048 tokens of 7168 with eight rows 99 and 79 us, 4096 of
+// 4096 with two 27.4 and 28.8, 8192 of it 52 and 54; with eight rows of 2048 the
+// CTA leads further on (4096 tokens: 52 and 48, 8192: 95 and 91).
+constexpr int kTokenWarps = 16;
 
 // 16 bytes: 8 values of bf16 or 4 of fp32.
 template <bool F32>

@@ -14,14 +14,19 @@
 // A token is read once and written to its k rows, so that x comes from memory
 // once; as MXFP4 it is quantised once.  Memory's writes bound the large calls
 // (16384 tokens of 2048 in bf16, eight of 128 experts each, 8.5 % dropped: 96 us,
-// 5.8 TB/s, of which the maps take 8.5; 4096 of 7168 as MXFP4: 40 us), launch
-// and the chain of prefix sums the small ones (64 tokens of 7168, eight of 256:
-// 4.6 us).
+// 5.8 TB/s, of which the maps take 8.5; 4096 of 7168 as MXFP4: 36 us, 5.1 TB/s,
+// the maps 6.5), launch and the chain of prefix sums the small ones (64 tokens of
+// 7168, eight of 256: 4.7 us).
 #include "mxfp4.cuh"
 
 namespace moe {
 namespace {
 
+// Assignments up to which one launch does it all.  One launch and three: 256
+// tokens of 7168, eight of 256 experts each, 9.9 and 10.7 us, 384 13.5 and 14.8,
+// 512 16.8 and 15.0 (as MXFP4 7.6 and 8.1, 10.6 and 9.7, 12.3 and 9.9); 256 of 2048
+// 7.0 and 7.6, 512 11.2 and 9.4; 1024 of 4096, two of 8, 8.0 and 8.6, 2048 13.3 and
+// 11.6.
 constexpr int kSmallRows = 2048;
 constexpr int kSmallThreads = 512;
 constexpr int kChunkRows = 256;  // assignments of a chunk at most (whole tokens)

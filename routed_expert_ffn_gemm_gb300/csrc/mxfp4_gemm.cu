@@ -282,12 +282,17 @@ moe_status launch(const Params& p, const Maps& maps, int num_sms, cudaStream_t s
 
 // From kMxManyRows rows an expert on average the product runs on
 // mxfp4_gemm_many.cu, up to kMxFewRows in tiles of 64 rows here, between in
-// tiles of 128.  64 experts of 7168 x 4096, us in tiles of 64, of 128 and there:
-// 16 rows 151, 154, 181; 48 rows 157, 158, 180; 64 rows 159, 160, 181 (spread
-// as rank^-0.6: 179, 170, 181); 96 rows 219, 173, 182; 128 rows 221, 187, 186
-// (277, 210, 192); 256 rows 424, 289, 196.  64 experts of 768 x 2048 with 128
-// rows: 46, 42, 30.  512 rows on 256 experts of 2048 x 7168: 288, 315, 346.  The
-// average counts experts without rows, which the host cannot see.
+// tiles of 128.  64 experts, us in tiles of 64, of 128 and there:
+//   rows              16            32            64            96            128           192
+//   7168 -> 4096  152 154 172   154 156 173   157 160 176   242 173 182   213 185 189   295 324 189
+//   2048 -> 4096   50  50  56    51  51  57    54  54  59    80  62  62    79  77  66   116 143  69
+//    768 -> 2048   16  18  21    16  18  19    24  25  19    41  32  21    41  40  22    57  74  24
+// (512 rows on 256 experts of 2048 x 7168: 288, 315, 346; 7168 -> 4096 spread as
+// rank^-0.6 with 64 rows on average: 179, 170, 181, with 128: 277, 210, 192.)  The
+// limit fits long reductions; with short ones the pair's kernel is ahead from some
+// 48 rows on (768 -> 2048: 22.7, 23.9, 21.0), which the rule leaves out.  The average
+// counts experts without rows, which the host cannot see: 16384 rows on 8 of 256
+// experts of 7168 -> 4096 take 261 us, on 8 of 8 147.
 constexpr long long kMxManyRows = 112, kMxFewRows = 32;
 
 moe_status mxfp4_gemm_launch(const MxGemmArgs& a, cudaStream_t s) {

@@ -17,6 +17,10 @@
 // copies write 37 KB and MMAs and scale copies read 35 KB, 560 cycles at 128
 // bytes a cycle; it takes 620 to 670 (16384 rows on 8 experts of 4096 -> 28672:
 // 585 us in bursts, 6.6 PFLOP/s, tensor pipe 73 % busy; 666 under the power cap).
+// A tile costs nearly the same whatever its rows: 64 experts of 7168 -> 4096 with
+// 256 rows each take 197 us, with 257 293, 384 316, 512 332.  Results in fp32 (twice
+// the stores): 65536 rows of 768 -> 2048 85 us in bf16 and 120 in fp32, 16384 rows
+// on 8 experts of 4096 -> 28672 608 and 753 (random codes).
 // The shared columns cost some 1000 cycles from a unit's last MMA to the next
 // one's first.  With few stages a unit the writing warps set the pace: 3300 of
 // 3900 cycles of a unit of three (65536 rows on 128 experts of 768 -> 2048: 76
